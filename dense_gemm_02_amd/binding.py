@@ -59,6 +59,19 @@ def load_library():
     L.gemm_fp8_scaled.restype = ci
     L.gemm_mxfp8.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, ci, vp]
     L.gemm_mxfp8.restype = ci
+    L.gemm_i8_scaled.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, ci, vp, i64, vp, i64, ci, vp]
+    L.gemm_i8_grouped.argtypes = [i64, i64, i64, i64, vp, i64, i64, vp, vp, i64, i64, vp, i64, ci, vp, i64, vp, i64,
+                                  vp, vp]
+    L.quantize_i8.argtypes = [i64, i64, vp, i64, ci, vp, i64, vp, vp]
+    L.expert_sort.argtypes = [i64, i64, i64, vp, ci, vp, vp, vp, vp, vp, i64, vp]
+    L.expert_dispatch.argtypes = [i64, i64, i64, ci, vp, i64, vp, vp, i64, i64, vp]
+    L.expert_combine.argtypes = [i64, i64, i64, ci, vp, i64, i64, vp, vp, vp, i64, vp]
+    L.expert_combine_grad.argtypes = [i64, i64, i64, ci, vp, i64, vp, i64, i64, vp, vp, vp, i64, vp, vp]
+    for name in ("gemm_i8_scaled", "gemm_i8_grouped", "quantize_i8", "expert_sort", "expert_dispatch",
+                 "expert_combine", "expert_combine_grad"):
+        getattr(L, name).restype = ci
+    L.expert_sort_workspace.argtypes = [i64, i64, i64]
+    L.expert_sort_workspace.restype = i64
     L.dgemm_last_hip_error.argtypes = []
     L.dgemm_last_hip_error.restype = ci
     L.dgemm_hip_error_string.argtypes = [ci]
@@ -275,7 +288,7 @@ def _dtype_name(t):
     return _TORCH_DT[t.dtype]
 
 
-def matmul(a, b, out=None, scale_a=None, scale_b=None, stream=None):
+def matmul(a, b, out=None, scale_a=None, scale_b=None, stream=None, out_dtype=None):
     """C = A x B for device tensors, the layout read from the strides.
 
     a: M x K row-major (stride(1) == 1).  b: K x N, either row-major (NN) or
@@ -284,9 +297,14 @@ def matmul(a, b, out=None, scale_a=None, scale_b=None, stream=None):
     for NN, column-major M x N (a transposed N x M tensor) for TN.  FP8
     (``torch.float8_e4m3fn``) returns float32; ``scale_a`` / ``scale_b``
     (float32 tensors of 1 or M / 1 or N values) select gemm_fp8_scaled.
+    int8 operands (``quantize_i8``) need both scale factors and give
+    ``out_dtype``: float32 (the default), float16 or bfloat16.
     ``out`` may be given with the same layout and dtype.
     """
     import torch
+    if isinstance(a, torch.Tensor) and a.dtype == torch.int8:
+        from .quantized import matmul_i8
+        return matmul_i8(a, b, scale_a, scale_b, out=out, out_dtype=out_dtype, stream=stream)
     for t in (a, b):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError("a and b must be device tensors")
@@ -307,6 +325,8 @@ def matmul(a, b, out=None, scale_a=None, scale_b=None, stream=None):
     else:
         raise ValueError("b must be row-major or column-major")
     odt = torch.float32 if dt in ("f32", "fp8") else a.dtype
+    if out_dtype not in (None, odt):
+        raise TypeError(f"{dt} operands give {odt}")
     if out is None:
         out = (torch.empty((M, N), dtype=odt, device=a.device) if layout == "nn"
                else torch.empty((N, M), dtype=odt, device=a.device).t())

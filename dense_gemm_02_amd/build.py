@@ -40,6 +40,9 @@ FOUR_WAVE = [
     ("fp8_tn", "OpFP8", 0), ("fp8_nn", "OpFP8", 1),
     ("fp8s_tn", "OpFP8S", 0), ("fp8s_nn", "OpFP8S", 1),
     ("mx8_tn", "OpMX8", 0), ("mx8_nn", "OpMX8", 1),
+    ("i8f_tn", "OpI8F", 0), ("i8f_nn", "OpI8F", 1),
+    ("i8h_tn", "OpI8H", 0), ("i8h_nn", "OpI8H", 1),
+    ("i8b_tn", "OpI8B", 0), ("i8b_nn", "OpI8B", 1),
 ]
 
 
@@ -47,6 +50,8 @@ def units():
     """(source, object, extra flags) of every translation unit."""
     out = [(os.path.join(CSRC, "dgemm.hip"), os.path.join(OBJDIR, "dgemm.o"), []),
            (os.path.join(CSRC, "pp.hip"), os.path.join(OBJDIR, "pp.o"), [])]
+    for name in ("i8", "grouped", "quantize", "experts"):
+        out.append((os.path.join(CSRC, name + ".hip"), os.path.join(OBJDIR, name + ".o"), []))
     for tag, op, nn in FOUR_WAVE:
         out.append((os.path.join(CSRC, "four_wave.hip"), os.path.join(OBJDIR, f"four_wave_{tag}.o"),
                     [f"-DDG_OP={op}", f"-DDG_PKM={nn}", f"-DDG_TAG={tag}", f"-DDG_FN=four_wave_{tag}"]))

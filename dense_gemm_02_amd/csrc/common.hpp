@@ -14,6 +14,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 // Number of XCDs on MI355X; workgroups are dispatched round-robin over them.
 constexpr int kXcds = 8;
@@ -154,5 +155,30 @@ struct GemmArgs {
   unsigned long long* trace;
   int64_t trace_n;
 };
+
+// Where a workgroup's tile index comes from: its place in the grid, or (a
+// grouped product, whose arguments are those of one tile) the only one.
+struct GridTile {
+  __device__ __forceinline__ int64_t operator()() const { return blockIdx.x; }
+};
+struct OneTile {
+  __device__ __forceinline__ int64_t operator()() const { return 0; }
+};
+
+// Rows of Q read through an index (grouped products): row q of the product
+// is row index[q] of Q's storage, which has `rows` rows; an index outside
+// them reads as a row of zeros.
+struct Gather {
+  const int32_t* index = nullptr;
+  int64_t rows = 0;
+};
+
+// Byte offset of 16-byte chunk `chunk` (a byte offset within the row) of the
+// row that row q < qn stands for; out of range where there is none.
+__device__ __forceinline__ uint32_t gather_row(const Gather& gt, int64_t q, int64_t qn, int64_t ld, int chunk) {
+  if (q >= qn) return kOobOffset;
+  const int32_t r = gt.index[q];
+  return (uint32_t)r < (uint32_t)gt.rows ? (uint32_t)(r * ld + chunk) : kOobOffset;
+}
 
 }  // namespace dg

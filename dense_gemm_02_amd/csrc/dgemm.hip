@@ -28,21 +28,16 @@ thread_local int g_last_hip_error = 0;
 thread_local unsigned long long* g_trace = nullptr;
 thread_local int64_t g_trace_n = 0;
 
-int hip_failed(hipError_t e) {
-  g_last_hip_error = (int)e;
-  return DGEMM_ERR_HIP;
-}
-
 // DT_FP8S: FP8 with scale factors (gemm_fp8_scaled); DT_MX8: MXFP8 with
-// E8M0 block scales (gemm_mxfp8).
-enum Dtype { DT_F32 = 0, DT_F16 = 1, DT_BF16 = 2, DT_FP8 = 3, DT_FP8S = 4, DT_MX8 = 5 };
+// E8M0 block scales (gemm_mxfp8); DT_I8 + t: int8 with scale factors and
+// results of dgemm_type t (gemm_i8_scaled).
+enum Dtype { DT_F32 = 0, DT_F16 = 1, DT_BF16 = 2, DT_FP8 = 3, DT_FP8S = 4, DT_MX8 = 5, DT_I8 = 6, DT_COUNT = 9 };
 
 bool is_fp8(int dt) { return dt == DT_FP8 || dt == DT_FP8S || dt == DT_MX8; }
+bool is_i8(int dt) { return dt >= DT_I8; }
 
-constexpr int64_t kMaxDescBytes = (int64_t(1) << 31) - 64;
-
-int in_elem(int dt) { return dt == DT_F32 ? 4 : (is_fp8(dt) ? 1 : 2); }
-int out_elem(int dt) { return (dt == DT_F32 || is_fp8(dt)) ? 4 : 2; }
+int in_elem(int dt) { return dt == DT_F32 ? 4 : (is_fp8(dt) || is_i8(dt) ? 1 : 2); }
+int out_elem(int dt) { return (dt == DT_F32 || is_fp8(dt) || dt == DT_I8 + DGEMM_F32) ? 4 : 2; }
 
 // ---- kernel table ------------------------------------------------------------
 // 16-bit and FP8: 256 x 256 block tile, 8 waves as 2 (p) x 4 (q), wave tile
@@ -133,7 +128,7 @@ int pick_tile(int64_t Pn, int64_t Qn, unsigned allowed, double* cost = nullptr) 
 // 256 x 192 only.
 unsigned tile_mask(int dt, bool nn, int64_t K) {
   const unsigned t192 = K < 4096 ? 0u : (nn ? 0b100000u : 0b110000u);
-  if (nn && is_fp8(dt)) return 0b0011u | t192;
+  if (nn && (is_fp8(dt) || is_i8(dt))) return 0b0011u | t192;
   return (dt == DT_MX8 ? 0b0101u : 0b1101u) | t192;
 }
 
@@ -178,8 +173,16 @@ Launch four_wave(int dt, bool nn, int idx, bool kt) {
     case DT_BF16: return nn ? four_wave_bf16_nn(idx, kt) : four_wave_bf16_tn(idx, kt);
     case DT_FP8S: return nn ? four_wave_fp8s_nn(idx, kt) : four_wave_fp8s_tn(idx, kt);
     case DT_MX8: return nn ? four_wave_mx8_nn(idx, kt) : four_wave_mx8_tn(idx, kt);
+    case DT_I8 + DGEMM_F32: return nn ? four_wave_i8f_nn(idx, kt) : four_wave_i8f_tn(idx, kt);
+    case DT_I8 + DGEMM_F16: return nn ? four_wave_i8h_nn(idx, kt) : four_wave_i8h_tn(idx, kt);
+    case DT_I8 + DGEMM_BF16: return nn ? four_wave_i8b_nn(idx, kt) : four_wave_i8b_tn(idx, kt);
     default: return nn ? four_wave_fp8_nn(idx, kt) : four_wave_fp8_tn(idx, kt);
   }
+}
+
+Launch ping_pong(int dt, bool kt) {
+  if (is_i8(dt)) return ping_pong_i8_tn(dt - DT_I8, kt);
+  return ping_pong_tn(dt == DT_F16 ? 0 : dt == DT_BF16 ? 1 : dt == DT_FP8 ? 2 : 3, kt);
 }
 
 // The kernel for kTiles entry `idx`: TN 256 x 256 tiles of FP16, BF16 and
@@ -188,8 +191,7 @@ Launch four_wave(int dt, bool nn, int idx, bool kt) {
 // 1550, FP16 1437 -> 1473, against the four-wave kernel); everything else
 // the four-wave kernel.
 Launch main_tile(int dt, bool nn, int idx, bool kt) {
-  if (idx == 0 && !nn && dt != DT_MX8)
-    return ping_pong_tn(dt == DT_F16 ? 0 : dt == DT_BF16 ? 1 : dt == DT_FP8 ? 2 : 3, kt);
+  if (idx == 0 && !nn && dt != DT_MX8) return ping_pong(dt, kt);
   return four_wave(dt, nn, idx, kt);
 }
 
@@ -228,7 +230,7 @@ bool forced_choice(int dt, bool nn, int64_t K, Choice* c) {
     return false;
   }
   const int e = in_elem(dt);
-  if (!(dt == DT_MX8 || (dt != DT_F32 && K % (16 / e) == 0 && K >= 2 * (128 / e)))) return false;
+  if (!(dt == DT_MX8 || is_i8(dt) || (dt != DT_F32 && K % (16 / e) == 0 && K >= 2 * (128 / e)))) return false;
   const bool kt = k_tail(dt, K);
   for (int idx = 0; idx < kNumTiles; ++idx) {
     const Launch L = four_wave(dt, nn, idx, kt);
@@ -238,7 +240,7 @@ bool forced_choice(int dt, bool nn, int64_t K, Choice* c) {
     }
   }
   if (!nn && dt != DT_MX8) {
-    const Launch L = ping_pong_tn(dt == DT_F16 ? 0 : dt == DT_BF16 ? 1 : dt == DT_FP8 ? 2 : 3, kt);
+    const Launch L = ping_pong(dt, kt);
     if (strcmp(L.name, want) == 0) {
       c->L = L;
       return true;
@@ -264,11 +266,11 @@ Choice choose(int dt, int layout, int64_t M, int64_t N, int64_t K) {
       return c;
     }
   }
-  // K a whole number of 16-byte chunks and at least two stages: the
-  // four-wave kernel (gemm_tn.hpp), tile chosen by shape; NN reads B with
+  // K a whole number of 16-byte chunks and at least two stages (int8: any
+  // K): the four-wave kernel (gemm_tn.hpp), tile chosen by shape; NN reads B with
   // transposing LDS reads.
   const int e = in_elem(dt);
-  if (dt == DT_MX8 || (dt != DT_F32 && K % (16 / e) == 0 && K >= 2 * (128 / e))) {
+  if (dt == DT_MX8 || is_i8(dt) || (dt != DT_F32 && K % (16 / e) == 0 && K >= 2 * (128 / e))) {
     const unsigned mask = tile_mask(dt, nn, K);
     double whole = 0.0;
     const int idx = pick_tile(Pn, Qn, mask, &whole);
@@ -425,7 +427,7 @@ int plan(int dt, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, co
     if (!l->p_trans && (int64_t)l->bp * g.ldp > kMaxDescBytes) return DGEMM_ERR_UNSUPPORTED;
     if (l->p_trans && K * g.ldp > kMaxDescBytes) return DGEMM_ERR_UNSUPPORTED;
   }
-  if (K * e > kMaxDescBytes) return DGEMM_ERR_UNSUPPORTED;
+  if (K * e > kMaxDescBytes || (is_i8(dt) && K > kMaxI8K)) return DGEMM_ERR_UNSUPPORTED;
   g.group = 8;
   const int oe = out_elem(dt);
   g.vec_store = ((((uintptr_t)C) % (uintptr_t)(4 * oe)) == 0 && ((ldc * oe) % (4 * oe)) == 0) ? 1 : 0;
@@ -470,13 +472,9 @@ int plan(int dt, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, co
   return DGEMM_OK;
 }
 
-// One launch on the caller's stream.
 int launch(const Launch& L, const GemmArgs& g, int64_t grid, void* stream) {
   GemmArgs arg = g;
-  void* args[] = {(void*)&arg};
-  const hipError_t err = hipLaunchKernel(L.fn, dim3((unsigned)grid), dim3(L.threads), args, 0, (hipStream_t)stream);
-  if (err != hipSuccess) return hip_failed(err);
-  return DGEMM_OK;
+  return launch_kernel(L.fn, grid, L.threads, &arg, stream);
 }
 
 int run(int dt, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B, int64_t ldb,
@@ -490,6 +488,12 @@ int run(int dt, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, con
 }
 
 }  // namespace
+
+int hip_failed(hipError_t e) {
+  g_last_hip_error = (int)e;
+  return DGEMM_ERR_HIP;
+}
+
 }  // namespace dg
 
 extern "C" {
@@ -535,6 +539,15 @@ int gemm_mxfp8(int64_t M, int64_t N, int64_t K, const uint8_t* A, int64_t lda, c
   return dg::run(dg::DT_MX8, M, N, K, A, lda, B, ldb, C, ldc, layout, stream, nullptr, &mx);
 }
 
+int gemm_i8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, void* C,
+                   int64_t ldc, int c_type, const float* scale_a, int64_t n_scale_a, const float* scale_b,
+                   int64_t n_scale_b, int layout, void* stream) {
+  if (layout != DGEMM_NN && layout != DGEMM_TN) return DGEMM_ERR_INVALID_LAYOUT;
+  if (c_type < DGEMM_F32 || c_type > DGEMM_BF16) return DGEMM_ERR_INVALID_TYPE;
+  const dg::Scales sc{scale_a, n_scale_a, scale_b, n_scale_b};
+  return dg::run(dg::DT_I8 + c_type, M, N, K, A, lda, B, ldb, C, ldc, layout, stream, &sc);
+}
+
 const char* gemm_strerror(int status) {
   switch (status) {
     case DGEMM_OK: return "success";
@@ -545,6 +558,7 @@ const char* gemm_strerror(int status) {
     case DGEMM_ERR_MISALIGNED: return "operand base or pitch not 16-byte aligned";
     case DGEMM_ERR_UNSUPPORTED: return "problem exceeds the supported size limits";
     case DGEMM_ERR_HIP: return "HIP launch error";
+    case DGEMM_ERR_INVALID_TYPE: return "element type not one the call takes";
     default: return "unknown status";
   }
 }
@@ -566,7 +580,7 @@ int64_t dgemm_lds_bytes(int bm, int bn, int bk, int elem, int pad_bytes, int buf
 }
 
 int dgemm_kernel_config(int dtype, int layout, int64_t M, int64_t N, int64_t K, char* buf, int64_t len) {
-  if (dtype < 0 || dtype > 5) return DGEMM_ERR_UNSUPPORTED;
+  if (dtype < 0 || dtype >= dg::DT_COUNT) return DGEMM_ERR_UNSUPPORTED;
   const int e = dg::in_elem(dtype);
   const bool nn = layout == DGEMM_NN;
   // Minimal legal, aligned leading dimensions for the description.

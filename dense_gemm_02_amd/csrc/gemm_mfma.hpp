@@ -44,7 +44,9 @@ struct OpF16 {
   static constexpr int OE = 2;     // bytes per output element
   static constexpr bool SCALED = false;  // scale factors applied in the epilogue
   static constexpr bool MX = false;      // E8M0 block scales fed to the MFMA
+  static constexpr bool TRIM = false;    // TN stages end at any K (else whole 16-byte chunks)
   typedef f16x8 Frag;
+  typedef f32x4 Acc16;    // accumulators of a 16 x 16 tile
   __device__ static Frag frag(const char* base, const uint32_t* off) { return *(const Frag*)(base + off[0]); }
   __device__ static f32x16 mma(Frag a, Frag b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
@@ -68,8 +70,9 @@ struct OpF16 {
 
 struct OpBF16 {
   static constexpr int ELEM = 2, KI = 16, FC = 1, OE = 2;
-  static constexpr bool SCALED = false, MX = false;
+  static constexpr bool SCALED = false, MX = false, TRIM = false;
   typedef bf16x8 Frag;
+  typedef f32x4 Acc16;
   __device__ static Frag frag(const char* base, const uint32_t* off) { return *(const Frag*)(base + off[0]); }
   __device__ static f32x16 mma(Frag a, Frag b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -90,8 +93,9 @@ struct OpBF16 {
 
 struct OpFP8 {
   static constexpr int ELEM = 1, KI = 64, FC = 2, OE = 4;
-  static constexpr bool SCALED = false, MX = false;
+  static constexpr bool SCALED = false, MX = false, TRIM = false;
   typedef i32x8 Frag;
+  typedef f32x4 Acc16;
   // 32 bytes of k per lane, read as two 16-byte (swizzled) chunks.
   __device__ static Frag frag(const char* base, const uint32_t* off) {
     const i32x4 lo = *(const i32x4*)(base + off[0]);
@@ -155,6 +159,38 @@ struct OpMX8 : OpFP8 {
   }
 };
 
+// Signed 8-bit integers with per-tensor or per-row scale factors: the sums
+// are exact in 32-bit integers (|a b| <= 2^14, so K <= 131071 cannot
+// overflow), converted to FP32 with one rounding and scaled like OpFP8S's.
+// A 32-byte fragment goes through two 16 x 16 x 64 MFMAs, one per 16-byte
+// chunk: the same bytes, and the same matrix rate, as one unscaled FP8 MFMA.
+// Which k a lane group holds does not matter as long as both operands agree,
+// so the FP8 chunk order stays.  Integers know no NaN, so one operand read
+// as zero past K is enough for any K: TN trims Q's straddling chunks in LDS
+// (TRIM), NN reads the rows of B past K as zeros anyway.
+template <class Out>
+struct OpI8 {
+  static constexpr int ELEM = 1, FC = 2, OE = Out::OE;
+  static constexpr bool SCALED = true, MX = false, TRIM = true;
+  typedef i32x4 Acc16;
+  __device__ static i32x4 mma16(const u32x4 (&a)[2], const u32x4 (&b)[2], i32x4 c) {
+    c = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a[0]), __builtin_bit_cast(i32x4, b[0]), c, 0, 0,
+                                              0);
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a[1]), __builtin_bit_cast(i32x4, b[1]), c, 0,
+                                                 0, 0);
+  }
+  __device__ static uint32_t pack2(float x, float y) { return Out::pack2(x, y); }
+  __device__ static uint16_t one(float x) { return Out::one(x); }
+};
+struct OutF32 {
+  static constexpr int OE = 4;
+  __device__ static uint32_t pack2(float, float) { return 0; }   // (FP32 results are stored as they are)
+  __device__ static uint16_t one(float) { return 0; }
+};
+struct OpI8F : OpI8<OutF32> {};   // FP32, FP16 and BF16 results
+struct OpI8H : OpI8<OpF16> {};
+struct OpI8B : OpI8<OpBF16> {};
+
 // Zero the bytes of a 16-byte chunk at and beyond `valid_bytes` (0..16).
 __device__ __forceinline__ u32x4 mask_tail(u32x4 v, int valid_bytes) {
 #pragma unroll
@@ -204,10 +240,27 @@ __device__ __forceinline__ void store4(const GemmArgs& a, int64_t q, int64_t p, 
 // whose factors it fetches per group.  Per-row factors are read through
 // buffer descriptors sized to the vectors, so a p or q past the edge reads 0
 // (never stored).
-template <int TQ, int MT = 32>
+//
+// GA: the rows of Q are read through an index (Gather); the factor of row q
+// is then that of the row it stands for.
+template <int TQ, int MT = 32, bool GA = false>
 struct EpiScale {
   float fq[TQ];
-  __device__ void init(const GemmArgs& a, int lane, int64_t qbase) {
+  __device__ void init(const GemmArgs& a, int lane, int64_t qbase, const Gather& gt) {
+    if constexpr (GA) {
+      // (Rows past the edge and rows with no source have factor 0.)
+      const __amdgpu_buffer_rsrc_t ri = make_rsrc(gt.index, (uint32_t)(a.Qn * 4));
+      const __amdgpu_buffer_rsrc_t rq = make_rsrc(a.sq, a.sq_row ? (uint32_t)(gt.rows * 4) : 4u);
+#pragma unroll
+      for (int j = 0; j < TQ; ++j) {
+        const int64_t q = qbase + MT * j + lane % MT;
+        const int r = __builtin_amdgcn_raw_buffer_load_b32(ri, (int)(q * 4), 0, 0);
+        const bool ok = q < a.Qn && (uint32_t)r < (uint32_t)gt.rows;
+        const uint32_t off = ok ? (a.sq_row ? (uint32_t)r * 4u : 0u) : kOobOffset;
+        fq[j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rq, (int)off, 0, 0));
+      }
+      return;
+    }
     if (a.sq_row) {
       const __amdgpu_buffer_rsrc_t rq = make_rsrc(a.sq, (uint32_t)(a.Qn * 4));
 #pragma unroll
@@ -258,9 +311,9 @@ struct EpiScale {
 // one write instruction covers 16 rows and four slots of each, keyed by
 // row mod 16 (measured: SQ_LDS_BANK_CONFLICT 0; the even key 2 (row mod 16),
 // which keeps 8-byte slot pairs in place, left 4 conflict cycles per write).
-template <class Op, int WTP, int WTQ, int TP, int TQ, int MT = 32, class AccT = f32x16>
+template <class Op, int WTP, int WTQ, int TP, int TQ, int MT = 32, class AccT = f32x16, bool GA = false>
 __device__ __forceinline__ void staged_epilogue(const GemmArgs& a, char* reg, const AccT (&acc)[TP][TQ], int lane,
-                                                int64_t pbase, int64_t qbase) {
+                                                int64_t pbase, int64_t qbase, const Gather& gt = Gather{}) {
   constexpr int OE = Op::OE;
   constexpr int PASSES = OE == 4 ? 2 : 1;
   constexpr int TPP = TP / PASSES;            // accumulator tiles along p per pass
@@ -273,8 +326,8 @@ __device__ __forceinline__ void staged_epilogue(const GemmArgs& a, char* reg, co
   static_assert(WTQ % 4 == 0, "four rows per read-back instruction");
   auto key = [](int row) { return MT == 32 ? row % NSL : row % 16; };
   const int lr = lane % MT, lg = lane / MT;
-  [[maybe_unused]] EpiScale<TQ, MT> sc;
-  if constexpr (Op::SCALED) sc.init(a, lane, qbase);
+  [[maybe_unused]] EpiScale<TQ, MT, GA> sc;
+  if constexpr (Op::SCALED) sc.init(a, lane, qbase, gt);
 #pragma unroll
   for (int pass = 0; pass < PASSES; ++pass) {
 #pragma unroll
@@ -282,10 +335,11 @@ __device__ __forceinline__ void staged_epilogue(const GemmArgs& a, char* reg, co
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         [[maybe_unused]] f32x4 fp;
-        if constexpr (Op::SCALED) fp = EpiScale<TQ, MT>::p4(a, pbase + MT * (pass * TPP + i) + 8 * g + 4 * lg);
+        if constexpr (Op::SCALED) fp = EpiScale<TQ, MT, GA>::p4(a, pbase + MT * (pass * TPP + i) + 8 * g + 4 * lg);
 #pragma unroll
         for (int j = 0; j < TQ; ++j) {
           const AccT& v = acc[pass * TPP + i][j];
+          // (integer sums convert to FP32 here, rounding to nearest-even)
           float v0 = v[4 * g], v1 = v[4 * g + 1], v2 = v[4 * g + 2], v3 = v[4 * g + 3];
           // 16 x 16: through vector registers (see the direct epilogue of
           // the four-wave kernel).

@@ -64,8 +64,8 @@ struct PpCfg {
 };
 
 // KT: K ends inside a stage, so the copies carry per-lane tail masks.
-template <class Op, bool KT>
-__device__ __forceinline__ void gemm_pp_body(const GemmArgs& a) {
+template <class Op, bool KT, class TileOf>
+__device__ __forceinline__ void gemm_pp_body(const GemmArgs& a, TileOf tile_of) {
   using Cfg = PpCfg<Op>;
   constexpr int E = Cfg::E, FC = Cfg::FC, ROWB = Cfg::ROWB, BK = Cfg::BK, CPE = Cfg::CPE;
   constexpr int TP = Cfg::TP, TQ = Cfg::TQ, MT = Cfg::MT, CPK = Cfg::CPK, KSTEPS = Cfg::KSTEPS;
@@ -81,7 +81,7 @@ __device__ __forceinline__ void gemm_pp_body(const GemmArgs& a) {
   const int nst = (int)((K + BK - 1) / BK);
   const uint32_t kbytes16 = (uint32_t)(((K * E) + 15) & ~(int64_t)15);
   const int64_t ntiles = a.tiles_p * a.tiles_q;
-  const int64_t tile = blockIdx.x;
+  const int64_t tile = tile_of();
   if (tile >= ntiles) return;   // (the whole workgroup)
 
   auto stamp = [&](int at) {
@@ -138,6 +138,21 @@ __device__ __forceinline__ void gemm_pp_body(const GemmArgs& a) {
           (cv0 + i * cstep) | kill, 0, 0, 0);
   };
 
+  // Any K (integers): the part of Q's chunks at and past K becomes zero once
+  // this wave's copies of the last stage have landed, before the barrier that
+  // publishes them.
+  constexpr bool TRIM = Op::TRIM && KT;
+  auto trim = [&](int t) {
+    const int left = (int)((K - (int64_t)t * BK) - dkc * CPE) * E;   // bytes of this lane's chunk below K
+    if (grp == 0 || left <= 0 || left >= 16) return;
+    char* sb = q_slot(t);
+#pragma unroll
+    for (int i = 0; i < Cfg::QSEG; ++i) {
+      u32x4* c = (u32x4*)(sb + (i * Cfg::NSIMD + simd) * 1024 + lane * 16);
+      *c = mask_tail(*c, left);
+    }
+  };
+
   // ---- fragments ----
   // Lane l holds row l % 16 of its P and Q tiles; lane group l / 16 selects
   // its k: 16-bit, chunk 4 kk + l / 16 of the stage row (8 k); FP8, chunks
@@ -163,11 +178,11 @@ __device__ __forceinline__ void gemm_pp_body(const GemmArgs& a) {
       }
   };
 
-  f32x4 acc[TP][TQ];
+  typename Op::Acc16 acc[TP][TQ];
 #pragma unroll
   for (int i = 0; i < TP; ++i)
 #pragma unroll
-    for (int j = 0; j < TQ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < TQ; ++j) acc[i][j] = typename Op::Acc16{0, 0, 0, 0};
   auto compute = [&]() {
 #pragma unroll
     for (int kk = 0; kk < KSTEPS; ++kk)
@@ -195,6 +210,9 @@ __device__ __forceinline__ void gemm_pp_body(const GemmArgs& a) {
   if (nst > 0) copies(0);
   if (grp == 1 && nst > 1) copies(1);
   __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+  if constexpr (TRIM) {
+    if (nst == 1 || nst == 2) trim(nst - 1);
+  }
   barrier();
   if (grp == 1) barrier();
   const int ahead = grp == 0 ? 1 : 2;   // stages ahead this group copies
@@ -208,13 +226,16 @@ __device__ __forceinline__ void gemm_pp_body(const GemmArgs& a) {
     // the wait ahead of them.)
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+    if constexpr (TRIM) {
+      if (t + 3 == nst) trim(t + 2);
+    }
     barrier();
   }
   if (grp == 0) barrier();
 
   // Epilogue: every wave is past its last LDS read; each stages its own
   // 64 rows of C (64 x 256 bytes) through LDS.
-  staged_epilogue<Op, Cfg::WTP, Cfg::WTQ, TP, TQ, MT, f32x4>(
+  staged_epilogue<Op, Cfg::WTP, Cfg::WTQ, TP, TQ, MT, typename Op::Acc16>(
       a, smem + wave * (Cfg::WTQ * 256), acc, lane, p0 + wp * Cfg::WTP,
       q0 + wq * (Cfg::BQ / 2) + grp * Cfg::WTQ);
   stamp(2);
@@ -223,7 +244,7 @@ __device__ __forceinline__ void gemm_pp_body(const GemmArgs& a) {
 template <class Op, bool KT>
 __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
 gemm_pp_kernel(const GemmArgs a) {
-  gemm_pp_body<Op, KT>(a);
+  gemm_pp_body<Op, KT>(a, GridTile{});
 }
 
 }  // namespace dg

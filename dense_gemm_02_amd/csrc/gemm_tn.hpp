@@ -54,7 +54,7 @@ struct TnCfg {
   static constexpr int MT = 16;
   static constexpr int KI = E == 2 ? 32 : 128;    // k per MFMA
   static constexpr int ACC = MT * MT / 64;         // accumulator registers per tile
-  using Acc = f32x4;
+  using Acc = typename Op::Acc16;
   static constexpr int TP = WTP / MT, TQ = WTQ / MT;
   static constexpr int KSTEPS = BK / KI;
   static constexpr int CPK = KI * E / 16;          // 16-byte chunks of k per k-step
@@ -115,8 +115,9 @@ struct TnCfg {
   static constexpr int WPE = TP * TQ * ACC <= 64 && NS == 2 ? 2 : 1;
 };
 
-template <class Op, bool PKM, int BP, int BQ, int NS, bool KT>
-__device__ __forceinline__ void gemm_tn_body(const GemmArgs& a) {
+// GA: row q of Q is row gt.index[q] of its storage.
+template <class Op, bool PKM, int BP, int BQ, int NS, bool KT, class TileOf, bool GA = false>
+__device__ __forceinline__ void gemm_tn_body(const GemmArgs& a, TileOf tile_of, const Gather& gt = Gather{}) {
   using Cfg = TnCfg<Op, PKM, BP, BQ, NS>;
   constexpr int NW = Cfg::NW, E = Cfg::E, FC = Cfg::FC, ROWB = Cfg::ROWB, BK = Cfg::BK, CPE = Cfg::CPE;
   constexpr int TP = Cfg::TP, TQ = Cfg::TQ, QSEG = Cfg::QSEG, NDMA = Cfg::NDMA;
@@ -145,8 +146,16 @@ __device__ __forceinline__ void gemm_tn_body(const GemmArgs& a) {
   const int dkc = (lane & 7) ^ ((4 * (wave_u & 1) + (lane >> 4)) & 7);
   const int dk0 = dkc * CPE;
   uint32_t qvo[QSEG], pvo[Cfg::PSEG];
+  if constexpr (GA) {
+    int64_t tp, tq;
+    tile_map(a.tiles_p, a.tiles_q, a.group, tile_of(), &tp, &tq);
 #pragma unroll
-  for (int i = 0; i < QSEG; ++i) qvo[i] = (uint32_t)((8 * (i * NW + wave_u) + (lane >> 3)) * a.ldq + dkc * 16);
+    for (int i = 0; i < QSEG; ++i)
+      qvo[i] = gather_row(gt, tq * Cfg::BQ + 8 * (i * NW + wave_u) + (lane >> 3), a.Qn, a.ldq, dkc * 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < QSEG; ++i) qvo[i] = (uint32_t)((8 * (i * NW + wave_u) + (lane >> 3)) * a.ldq + dkc * 16);
+  }
   if constexpr (!PKM) {
 #pragma unroll
     for (int i = 0; i < Cfg::PSEG; ++i)
@@ -183,8 +192,8 @@ __device__ __forceinline__ void gemm_tn_body(const GemmArgs& a) {
       const int64_t q0 = tq * Cfg::BQ, p0 = tp * Cfg::BP;
       const int64_t qrows = (a.Qn - q0) < Cfg::BQ ? (a.Qn - q0) : Cfg::BQ;
       const int64_t prows = (a.Pn - p0) < Cfg::BP ? (a.Pn - p0) : Cfg::BP;
-      r.q = a.Q + q0 * a.ldq;
-      r.qn = (uint32_t)((qrows - 1) * a.ldq) + kbytes16;
+      r.q = GA ? a.Q : a.Q + q0 * a.ldq;
+      r.qn = (uint32_t)(((GA ? gt.rows : qrows) - 1) * a.ldq) + kbytes16;
       if constexpr (Op::MX) {
         // The caller provides rows * ld scale bytes; with K == 0 none at all.
         r.sq = a.msq + q0 * a.ldsq;
@@ -332,7 +341,7 @@ __device__ __forceinline__ void gemm_tn_body(const GemmArgs& a) {
 #pragma unroll
       for (int j = 0; j < TQ; ++j)
 #pragma unroll
-        for (int r = 0; r < Cfg::ACC; ++r) acc[i][j][r] = 0.0f;
+        for (int r = 0; r < Cfg::ACC; ++r) acc[i][j][r] = 0;
   };
   // MX block scales: for the stage in use, lane l holds in scp[i] / scq[j]
   // the scale of its row of P tile i / Q tile j for block lg of the stage (a
@@ -422,6 +431,21 @@ __device__ __forceinline__ void gemm_tn_body(const GemmArgs& a) {
   // Stream position g + NS (the copies after the barrier of stage g).
   auto pos_far = [&](int s, const Src& cu) -> Pos { return pos_at(cu, s + NS, s + NS < nst); };
 
+  // TRIM: once this wave's copies of the last stage t have landed, the part
+  // of Q's chunks at and past K becomes zero (the next barrier publishes it).
+  constexpr bool TRIM = Op::TRIM && KT && !PKM;
+  auto trim = [&](int t) {
+    const int left = (int)((K - (int64_t)t * BK) - dk0) * E;   // bytes of this lane's chunk below K
+    if (K % CPE == 0) return;
+    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+    if (left <= 0 || left >= 16) return;
+#pragma unroll
+    for (int i = 0; i < QSEG; ++i) {
+      u32x4* c = (u32x4*)(smem + (t & (NS - 1)) * Cfg::STAGE + Cfg::P_LDS + (i * NW + wave_u) * 1024 + lane * 16);
+      *c = mask_tail(*c, left);
+    }
+  };
+
   // ---- one stage, rolling (one k-step per stage) ----
   // Phase 1, before the barrier: P tiles 0 .. HP-1 against every Q tile,
   // Q-major, while P tiles HP .. TP-1 of this stage are read (their
@@ -446,6 +470,12 @@ __device__ __forceinline__ void gemm_tn_body(const GemmArgs& a) {
     if constexpr (Op::MX) {
       if (gpend) copy_group(gpend_src, gpend_g, gpend_buf);
       take_scales(s, nsp, nsq);
+    }
+    if constexpr (TRIM) {
+      // (All copies of the last stage have been issued: none are left for
+      // the slots before the barrier.)
+      static_assert(NB == 0, "every copy of a stage goes out before the stage ahead of it");
+      if (s + 2 == nst) trim(s + 1);
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -537,7 +567,7 @@ __device__ __forceinline__ void gemm_tn_body(const GemmArgs& a) {
   };
 
   // ---- tiles ----
-  const int64_t tile = blockIdx.x;
+  const int64_t tile = tile_of();
   if (tile >= ntiles) return;
   // Clock trace: the start stamps go out now, so that nothing of the trace
   // stays live across the stage loop.
@@ -575,6 +605,9 @@ __device__ __forceinline__ void gemm_tn_body(const GemmArgs& a) {
     // Position 0 has landed once at most the copies of positions 1 .. NS-1
     // are open.
     __builtin_amdgcn_s_waitcnt(kWaitVmcntBase | vmcnt_bits(Cfg::VM_MID + NA));
+    if constexpr (TRIM) {
+      if (nst == 1) trim(0);
+    }
     __syncthreads();
     if constexpr (Op::MX) read_scales(0, 0);
     // Stage 0's first fragments: all of them, or (rolling) the Q tiles and
@@ -594,8 +627,8 @@ __device__ __forceinline__ void gemm_tn_body(const GemmArgs& a) {
     int64_t tp, tq;
     tile_map(a.tiles_p, a.tiles_q, a.group, t, &tp, &tq);
     const int64_t pb = tp * Cfg::BP + wp * Cfg::WTP, qb = tq * Cfg::BQ + wq * Cfg::WTQ;
-    [[maybe_unused]] EpiScale<TQ, MT> sc;
-    if constexpr (Op::SCALED) sc.init(a, lane_id(), qb);
+    [[maybe_unused]] EpiScale<TQ, MT, GA> sc;
+    if constexpr (Op::SCALED) sc.init(a, lane_id(), qb, gt);
     // Column by column: a lane's four stores into one column of C follow
     // each other, so each 128-byte line is written whole while it is open.
 #pragma unroll
@@ -603,7 +636,7 @@ __device__ __forceinline__ void gemm_tn_body(const GemmArgs& a) {
       [[maybe_unused]] f32x4 fp[NG];
       if constexpr (Op::SCALED) {
 #pragma unroll
-        for (int gg = 0; gg < NG; ++gg) fp[gg] = EpiScale<TQ, MT>::p4(a, pb + MT * i + 8 * gg + 4 * lg);
+        for (int gg = 0; gg < NG; ++gg) fp[gg] = EpiScale<TQ, MT, GA>::p4(a, pb + MT * i + 8 * gg + 4 * lg);
       }
 #pragma unroll
       for (int j = 0; j < TQ; ++j) {
@@ -646,8 +679,9 @@ __device__ __forceinline__ void gemm_tn_body(const GemmArgs& a) {
     int64_t tp, tq;
     tile_map(a.tiles_p, a.tiles_q, a.group, tile, &tp, &tq);
     static_assert(!Cfg::STAGED_EPI || Cfg::WTQ * 256 * NW <= 2 * Cfg::STAGE, "staging fits in the stage buffers");
-    staged_epilogue<Op, Cfg::WTP, Cfg::WTQ, TP, TQ, MT, Acc>(a, smem + wave_u * (Cfg::WTQ * 256), acc, lane_id(),
-                                                             tp * Cfg::BP + wp * Cfg::WTP, tq * Cfg::BQ + wq * Cfg::WTQ);
+    staged_epilogue<Op, Cfg::WTP, Cfg::WTQ, TP, TQ, MT, Acc, GA>(
+        a, smem + wave_u * (Cfg::WTQ * 256), acc, lane_id(), tp * Cfg::BP + wp * Cfg::WTP,
+        tq * Cfg::BQ + wq * Cfg::WTQ, gt);
   } else {
     direct_epilogue(tile);
   }
@@ -659,7 +693,7 @@ template <class Op, bool PKM, int BP, int BQ, int NS, bool KT>
 __global__ void __launch_bounds__(256)
 __attribute__((amdgpu_waves_per_eu(TnCfg<Op, PKM, BP, BQ, NS>::WPE, TnCfg<Op, PKM, BP, BQ, NS>::WPE)))
 gemm_tn_kernel(const GemmArgs a) {
-  gemm_tn_body<Op, PKM, BP, BQ, NS, KT>(a);
+  gemm_tn_body<Op, PKM, BP, BQ, NS, KT>(a, GridTile{});
 }
 
 }  // namespace dg

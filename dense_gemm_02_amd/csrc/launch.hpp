@@ -39,4 +39,30 @@ Launch four_wave_mx8_nn(int idx, bool kt);
 // 1 BF16, 2 FP8, 3 FP8 with scale factors.
 Launch ping_pong_tn(int op, bool kt);
 
+// Int8 with FP32, FP16 and BF16 results (any K).
+Launch four_wave_i8f_tn(int idx, bool kt);
+Launch four_wave_i8f_nn(int idx, bool kt);
+Launch four_wave_i8h_tn(int idx, bool kt);
+Launch four_wave_i8h_nn(int idx, bool kt);
+Launch four_wave_i8b_tn(int idx, bool kt);
+Launch four_wave_i8b_nn(int idx, bool kt);
+Launch ping_pong_i8_tn(int out, bool kt);   // out: dgemm_type
+
+// Keeps a HIP failure for dgemm_last_hip_error and returns DGEMM_ERR_HIP.
+int hip_failed(hipError_t e);
+
+// A buffer descriptor covers less than 2^31 bytes.
+constexpr int64_t kMaxDescBytes = (int64_t(1) << 31) - 64;
+
+// The sum of K products of two int8 values fits 32 bits up to this K.
+constexpr int64_t kMaxI8K = 131071;
+
+// One launch on the caller's stream.
+inline int launch_kernel(const void* fn, int64_t grid, int threads, void* arg, void* stream) {
+  void* args[] = {arg};
+  const hipError_t err = hipLaunchKernel(fn, dim3((unsigned)grid), dim3((unsigned)threads), args, 0,
+                                         (hipStream_t)stream);
+  return err == hipSuccess ? 0 : hip_failed(err);
+}
+
 }  // namespace dg

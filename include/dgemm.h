@@ -71,8 +71,12 @@ typedef enum {
   DGEMM_ERR_INVALID_LAYOUT = 4,
   DGEMM_ERR_MISALIGNED = 5,
   DGEMM_ERR_UNSUPPORTED = 6,
-  DGEMM_ERR_HIP = 7
+  DGEMM_ERR_HIP = 7,
+  DGEMM_ERR_INVALID_TYPE = 8
 } dgemm_status;
+
+/* Element types of the operators that take more than one. */
+typedef enum { DGEMM_F32 = 0, DGEMM_F16 = 1, DGEMM_BF16 = 2 } dgemm_type;
 
 /* FP32 x FP32 -> FP32. */
 int gemm_f32(int64_t M, int64_t N, int64_t K, const float* A, int64_t lda,
@@ -139,6 +143,123 @@ int gemm_mxfp8(int64_t M, int64_t N, int64_t K, const uint8_t* A, int64_t lda,
                const uint8_t* scale_a, int64_t ldsa, const uint8_t* scale_b, int64_t ldsb,
                int layout, void* stream);
 
+/*
+ * int8 x int8 -> FP32, FP16 or BF16 with scale factors (a linear layer
+ * quantized symmetrically, one factor per token and per output channel):
+ *   C_ij = (sum_k A_ik * B_kj) * (sa_i * sb_j)
+ * The sum is exact in 32-bit integers (all 256 values of a byte are allowed),
+ * converted to FP32 (one rounding), multiplied in FP32 as in gemm_fp8_scaled
+ * and rounded once more to c_type (a dgemm_type; ldc counts elements of it).
+ * K above 131071, where a sum could leave 32 bits, -> DGEMM_ERR_UNSUPPORTED.
+ * A c_type that is none -> DGEMM_ERR_INVALID_TYPE (checked after the layout).
+ * Factors and all other arguments and checks as gemm_fp8_scaled.
+ */
+int gemm_i8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda,
+                   const int8_t* B, int64_t ldb, void* C, int64_t ldc, int c_type,
+                   const float* scale_a, int64_t n_scale_a, const float* scale_b, int64_t n_scale_b,
+                   int layout, void* stream);
+
+/*
+ * The int8 products of a mixture of experts: `rows` tokens sorted by group
+ * (expert), group e's at rows offsets[e] .. offsets[e + 1] - 1 of C, each
+ * multiplied with its group's weights.  All row-major:
+ *   C[n*ldc + j] = (sum_k A[r*lda + k] * B[e*group_b + j*ldb + k]) * (sa_r * sb_ej)
+ * with r = n, or r = row_index[n] where row_index is given (rows of A in
+ * another order, each as often as wanted).  Sums, factors, rounding and
+ * c_type as gemm_i8_scaled.
+ * A: rows_a x K, lda >= K.  B: `groups` matrices of N x K, ldb >= K, group_b
+ * elements apart (0: one matrix for every group).  C: rows x N, ldc >= N.
+ * offsets: DEVICE pointer to groups + 1 values, ascending, within 0 .. rows
+ * (read by the kernel; values outside are clamped).  Rows of C before the
+ * first and behind the last group are left as they were, a group may be empty.
+ * row_index: DEVICE pointer to `rows` values or NULL (then rows_a >= rows is
+ * required); a row whose index is outside 0 .. rows_a - 1 counts as zeros
+ * with the factor 0.
+ * scale_a: n_scale_a = 1 or rows_a values; scale_b: n_scale_b = 1 or
+ * groups*N values, scale_b[e*N + j].
+ * A and B must be 16-byte aligned with lda, ldb and group_b multiples of 16,
+ * A readable over rows_a*lda and B over (groups - 1)*group_b + N*ldb bytes;
+ * offsets, row_index and the factors 4-byte, C element-aligned.
+ * Checks, in this order: c_type; negative extents or group_b ->
+ * DGEMM_ERR_INVALID_DIM; groups, N or groups*N above 2^31 - 1 ->
+ * DGEMM_ERR_UNSUPPORTED; factor counts, rows_a against rows ->
+ * DGEMM_ERR_INVALID_DIM; rows == 0, N == 0 or groups == 0 -> DGEMM_OK with no
+ * work; NULL pointers (A and B may be NULL if K == 0, A and
+ * scale_a if rows_a == 0); leading dimensions;
+ * alignment; limits -> DGEMM_ERR_UNSUPPORTED: K above 131071; 256*lda, 256*ldb,
+ * 4*rows, 4*rows_a, 4*N or (with row_index) rows_a*lda at or above 2^31.
+ */
+int gemm_i8_grouped(int64_t groups, int64_t rows, int64_t N, int64_t K, const int8_t* A, int64_t rows_a, int64_t lda,
+                    const int32_t* row_index, const int8_t* B, int64_t ldb, int64_t group_b, void* C, int64_t ldc,
+                    int c_type, const float* scale_a, int64_t n_scale_a, const float* scale_b, int64_t n_scale_b,
+                    const int32_t* offsets, void* stream);
+
+/*
+ * Rows to int8 with one factor per row, as the products above take them:
+ *   scale[i] = fl(max_k |x_ik| / 127),  Q_ik = round(x_ik / scale[i])
+ * with the quotient taken exactly and rounded to nearest-even, in -127 .. 127.
+ * A row of zeros (or one so small that scale[i] rounds to 0) gets scale 0
+ * and zeros; a row that holds an infinity or NaN gets that as its scale and
+ * zeros, so that its products are NaN.  K == 0: scale 0.
+ * X: rows x K row-major of type x_type, ldx >= K; Q: ldq >= K.  No alignment
+ * beyond that of the elements; elements of Q past K in a row are left.
+ * Checks: x_type; negative sizes -> DGEMM_ERR_INVALID_DIM; rows == 0 ->
+ * DGEMM_OK; NULL pointers (X and Q may be NULL if K == 0); leading
+ * dimensions; alignment; rows above 2^31 - 1 -> DGEMM_ERR_UNSUPPORTED.
+ */
+int quantize_i8(int64_t rows, int64_t K, const void* X, int64_t ldx, int x_type, int8_t* Q, int64_t ldq,
+                float* scale, void* stream);
+
+/*
+ * Tokens sorted by expert and back (mixture of experts).  A pair (t, j) is
+ * choice j of token t; `tokens` x k of them, numbered t*k + j.
+ *
+ * expert_sort: a stable counting sort of the pairs by ids[t*k + j] (64- or
+ * 32-bit integers, id_bytes = 8 or 4).  A pair whose id is outside 0 ..
+ * experts - 1 is dropped.  Writes
+ *   offsets[e]      number of pairs of experts below e; experts + 1 values
+ *   slot[t*k + j]   the pair's place in the sorted order, -1 if dropped
+ *   pair[n]         the pair at place n, -1 behind the last one
+ *   token[n]        its token, pair[n] / k, -1 behind the last one (may be
+ *                   NULL: not wanted; the row_index of gemm_i8_grouped)
+ * all DEVICE arrays of 32-bit integers.  The order within an expert is that
+ * of the pairs.  workspace: expert_sort_workspace(tokens, k, experts) bytes
+ * of DEVICE memory (0: may be NULL), 4-byte aligned, free again once the call's
+ * work on the stream is done; too few bytes -> DGEMM_ERR_INVALID_DIM.
+ * experts <= 1024 and tokens*k <= 2^31 - 1, else DGEMM_ERR_UNSUPPORTED (the
+ * workspace query then returns -1).
+ *
+ * expert_dispatch: Y[slot[t*k + j]] = X[t] for every pair (rows of H values);
+ * rows of Y that no slot names are left as they were.
+ * expert_combine: O[t] = sum_j w[t*k + j] * Y[slot[t*k + j]], in the order of
+ * j in FP32 and rounded once; weights == NULL: all 1, which is the gradient
+ * of expert_dispatch.  A token with no pair gets zeros.
+ * expert_combine_grad, the gradients of expert_combine:
+ *   dY[slot[t*k + j]] = w[t*k + j] * dO[t],  dW[t*k + j] = dO[t] . Y[slot[t*k + j]]
+ * (FP32, 0 for a dropped pair); rows of dY that no slot names are left.
+ * weights == NULL: all 1; dW == NULL: not wanted (Y is then not read and may
+ * be NULL); dY == NULL likewise.  dY must not overlap Y or dO.
+ * In all three a slot outside 0 .. rows - 1 (rows: of Y and dY) counts as
+ * dropped; a slot must not occur twice where rows are written.  `type` is the
+ * dgemm_type of every row matrix; pitches are in elements, at least H; no
+ * alignment beyond that of the elements.  Results do not depend on timing:
+ * no atomics are used.
+ * Checks: type (id_bytes); negative sizes -> DGEMM_ERR_INVALID_DIM; nothing
+ * to do -> DGEMM_OK; NULL pointers; leading dimensions; alignment; limits
+ * (tokens*k or rows above 2^31 - 1 -> DGEMM_ERR_UNSUPPORTED).
+ */
+int64_t expert_sort_workspace(int64_t tokens, int64_t k, int64_t experts);
+int expert_sort(int64_t tokens, int64_t k, int64_t experts, const void* ids, int id_bytes, int32_t* offsets,
+                int32_t* slot, int32_t* pair, int32_t* token, void* workspace, int64_t workspace_bytes,
+                void* stream);
+int expert_dispatch(int64_t tokens, int64_t k, int64_t H, int type, const void* X, int64_t ldx, const int32_t* slot,
+                    void* Y, int64_t rows, int64_t ldy, void* stream);
+int expert_combine(int64_t tokens, int64_t k, int64_t H, int type, const void* Y, int64_t rows, int64_t ldy,
+                   const int32_t* slot, const float* weights, void* O, int64_t ldo, void* stream);
+int expert_combine_grad(int64_t tokens, int64_t k, int64_t H, int type, const void* dO, int64_t ldo, const void* Y,
+                        int64_t rows, int64_t ldy, const int32_t* slot, const float* weights, void* dY, int64_t lddy,
+                        float* dW, void* stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* gemm_strerror(int status);
 
@@ -168,7 +289,8 @@ const char* dgemm_hip_error_string(int code);
  * dgemm_kernel_config: writes a one-line description (kernel name, tile, wave
  * grid, LDS bytes, grid size) of the kernel a call with these arguments would
  * launch into buf (at most len bytes, NUL-terminated).  dtype: 0 f32, 1 f16,
- * 2 bf16, 3 fp8, 4 fp8 with scale factors, 5 MXFP8.  Returns 0, or a
+ * 2 bf16, 3 fp8, 4 fp8 with scale factors, 5 MXFP8, 6 / 7 / 8 int8 with
+ * FP32 / FP16 / BF16 results.  Returns 0, or a
  * dgemm_status for invalid arguments.
  */
 /*

@@ -1,0 +1,176 @@
+"""Host-only checks of the int8 and expert entry points: every refusal the
+header documents, in its order, before anything touches the GPU, and what the
+Python functions refuse.  No kernel is launched here."""
+
+import os
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from dense_gemm_02_amd import binding
+    if not os.path.exists(binding.library_path()):
+        from dense_gemm_02_amd import build
+        build.build()
+    return binding.load_library()
+
+
+FAKE = 1 << 20            # aligned fake device address; never dereferenced here
+OK, DIM, NULL, LD, LAYOUT, ALIGN, UNSUP, TYPE = 0, 1, 2, 3, 4, 5, 6, 8
+
+
+def i8(lib, M=4, N=5, K=32, A=FAKE, lda=32, B=FAKE, ldb=32, C=FAKE, ldc=5, c=0, sa=FAKE, na=4, sb=FAKE, nb=5, layout=1):
+    return lib.gemm_i8_scaled(M, N, K, A, lda, B, ldb, C, ldc, c, sa, na, sb, nb, layout, None)
+
+
+def test_i8_scaled_refusals(lib):
+    assert i8(lib, layout=2, c=9, M=-1) == LAYOUT
+    for c in (-1, 3):
+        assert i8(lib, c=c, M=-1) == TYPE
+    assert i8(lib, M=-1) == DIM and i8(lib, N=-1) == DIM and i8(lib, K=-1) == DIM
+    assert i8(lib, na=3) == DIM and i8(lib, nb=0) == DIM and i8(lib, M=0, na=3) == DIM
+    assert i8(lib, M=0, na=0, A=None, lda=0) == OK and i8(lib, N=0, nb=1, C=None) == OK
+    assert i8(lib, A=None) == NULL and i8(lib, B=None) == NULL and i8(lib, C=None) == NULL
+    assert i8(lib, sa=None) == NULL and i8(lib, sb=None) == NULL
+    assert i8(lib, lda=16) == LD and i8(lib, ldb=16) == LD and i8(lib, ldc=3) == LD
+    assert i8(lib, layout=0, ldb=4) == LD and i8(lib, layout=0, ldc=4) == LD
+    assert i8(lib, A=FAKE + 8) == ALIGN and i8(lib, B=FAKE + 1) == ALIGN and i8(lib, lda=40) == ALIGN
+    assert i8(lib, ldb=33) == ALIGN and i8(lib, C=FAKE + 2) == ALIGN and i8(lib, C=FAKE + 1, c=1) == ALIGN
+    assert i8(lib, sa=FAKE + 2) == ALIGN and i8(lib, sb=FAKE + 1) == ALIGN
+    assert i8(lib, K=131072, lda=131072, ldb=131072) == UNSUP
+    assert i8(lib, M=300, na=300, lda=1 << 24, ldc=300) == UNSUP
+
+
+def test_i8_kernel_choice(lib):
+    import ctypes
+    buf = ctypes.create_string_buffer(256)
+
+    def name(t, layout, M, N, K):
+        assert lib.dgemm_kernel_config(6 + t, layout, M, N, K, buf, 256) == 0
+        return buf.value.decode().split()[0]
+
+    for t, tag in ((0, "i8f"), (1, "i8h"), (2, "i8b")):
+        assert name(t, 1, 8192, 8192, 8192) == f"{tag}_tn_256x256_pp"
+        assert name(t, 0, 8192, 8192, 8192) == f"{tag}_nn_256x256_w4"
+        for layout in (0, 1):
+            for K in (0, 1, 17, 4111):
+                assert name(t, layout, 300, 260, K).startswith(f"{tag}_{'tn' if layout else 'nn'}")
+    assert lib.dgemm_kernel_config(9, 1, 4, 4, 4, buf, 256) == UNSUP
+
+
+def grouped(lib, G=3, rows=10, N=20, K=32, A=FAKE, ra=10, lda=32, idx=None, B=FAKE, ldb=32, gb=640, C=FAKE, ldc=20,
+            c=2, sa=FAKE, na=10, sb=FAKE, nb=60, off=FAKE):
+    return lib.gemm_i8_grouped(G, rows, N, K, A, ra, lda, idx, B, ldb, gb, C, ldc, c, sa, na, sb, nb, off, None)
+
+
+def test_grouped_refusals(lib):
+    assert grouped(lib, c=3, G=-1) == TYPE and grouped(lib, c=-1) == TYPE
+    for kw in (dict(G=-1), dict(rows=-1), dict(N=-1), dict(K=-1), dict(ra=-1), dict(gb=-16)):
+        assert grouped(lib, **kw) == DIM
+    assert grouped(lib, G=1 << 31, nb=1) == UNSUP and grouped(lib, N=1 << 31, nb=1) == UNSUP
+    assert grouped(lib, G=1 << 16, N=1 << 16, nb=1) == UNSUP
+    assert grouped(lib, na=9) == DIM and grouped(lib, nb=20) == DIM
+    assert grouped(lib, ra=9, na=9) == DIM
+    assert grouped(lib, rows=0, A=None) == OK and grouped(lib, N=0, nb=0) == OK
+    assert grouped(lib, G=0, nb=0, off=None) == OK
+    for kw in (dict(A=None), dict(B=None), dict(C=None), dict(sa=None), dict(sb=None), dict(off=None)):
+        assert grouped(lib, **kw) == NULL
+    assert grouped(lib, lda=16) == LD and grouped(lib, ldb=16) == LD and grouped(lib, ldc=19) == LD
+    for kw in (dict(A=FAKE + 4), dict(B=FAKE + 8), dict(lda=40), dict(ldb=36), dict(gb=641), dict(C=FAKE + 1),
+               dict(sa=FAKE + 1), dict(sb=FAKE + 2), dict(off=FAKE + 2), dict(idx=FAKE + 1)):
+        assert grouped(lib, **kw) == ALIGN
+    assert grouped(lib, K=131072, lda=131072, ldb=131072) == UNSUP
+    assert grouped(lib, lda=1 << 23) == UNSUP and grouped(lib, ldb=1 << 23) == UNSUP
+    # with an index every row of A is within one descriptor
+    assert grouped(lib, idx=FAKE, ra=1 << 20, na=1, lda=1 << 11) == UNSUP
+
+
+def quantize(lib, rows=4, K=10, X=FAKE, ldx=10, t=2, Q=FAKE, ldq=10, s=FAKE):
+    return lib.quantize_i8(rows, K, X, ldx, t, Q, ldq, s, None)
+
+
+def test_quantize_refusals(lib):
+    assert quantize(lib, t=3, rows=-1) == TYPE and quantize(lib, t=-1) == TYPE
+    assert quantize(lib, rows=-1) == DIM and quantize(lib, K=-1) == DIM
+    assert quantize(lib, rows=0, X=None, Q=None, s=None) == OK
+    assert quantize(lib, X=None) == NULL and quantize(lib, Q=None) == NULL and quantize(lib, s=None) == NULL
+    assert quantize(lib, K=0, X=None, Q=None, s=None) == NULL
+    assert quantize(lib, ldx=9) == LD and quantize(lib, ldq=9) == LD
+    assert quantize(lib, X=FAKE + 1) == ALIGN and quantize(lib, X=FAKE + 2, t=0) == ALIGN
+    assert quantize(lib, s=FAKE + 2) == ALIGN
+    assert quantize(lib, rows=1 << 31) == UNSUP
+
+
+def sort(lib, T=6, k=2, E=4, ids=FAKE, b=8, off=FAKE, slot=FAKE, pair=FAKE, tok=None, ws=FAKE, n=1 << 40):
+    return lib.expert_sort(T, k, E, ids, b, off, slot, pair, tok, ws, n, None)
+
+
+def test_sort_refusals(lib):
+    assert sort(lib, b=2, T=-1) == TYPE
+    assert sort(lib, T=-1) == DIM and sort(lib, k=-1) == DIM and sort(lib, E=-1) == DIM
+    assert sort(lib, E=1025) == UNSUP and sort(lib, T=1 << 30, k=2) == UNSUP and sort(lib, T=1 << 40, k=1 << 40) == UNSUP
+    assert sort(lib, n=-1) == DIM
+    for kw in (dict(ids=None), dict(off=None), dict(slot=None), dict(pair=None)):
+        assert sort(lib, **kw) == NULL
+    for kw in (dict(ids=FAKE + 4), dict(off=FAKE + 1), dict(slot=FAKE + 2), dict(pair=FAKE + 1), dict(tok=FAKE + 3)):
+        assert sort(lib, **kw) == ALIGN
+    assert sort(lib, ids=FAKE + 2, b=4) == ALIGN
+    ask = lib.expert_sort_workspace
+    assert ask(-1, 2, 4) == -1 and ask(4, 2, 1025) == -1 and ask(1 << 30, 2, 4) == -1
+    for T, k, E in ((0, 1, 1), (16, 8, 64), (100000, 8, 1024), (1 << 28, 1, 7)):
+        need = ask(T, k, E)
+        assert need >= 0
+        if need > 0:
+            assert sort(lib, T=T, k=k, E=E, n=need - 1) == DIM
+            assert sort(lib, T=T, k=k, E=E, ws=None) == NULL
+            assert sort(lib, T=T, k=k, E=E, ws=FAKE + 2) == ALIGN
+
+
+def test_row_operator_refusals(lib):
+    def dispatch(T=3, k=2, H=8, t=2, X=FAKE, ldx=8, slot=FAKE, Y=FAKE, rows=6, ldy=8):
+        return lib.expert_dispatch(T, k, H, t, X, ldx, slot, Y, rows, ldy, None)
+
+    def combine(T=3, k=2, H=8, t=2, Y=FAKE, rows=6, ldy=8, slot=FAKE, w=FAKE, O=FAKE, ldo=8):
+        return lib.expert_combine(T, k, H, t, Y, rows, ldy, slot, w, O, ldo, None)
+
+    def grad(T=3, k=2, H=8, t=2, dO=FAKE, ldo=8, Y=FAKE, rows=6, ldy=8, slot=FAKE, w=FAKE, dY=FAKE, lddy=8, dW=FAKE):
+        return lib.expert_combine_grad(T, k, H, t, dO, ldo, Y, rows, ldy, slot, w, dY, lddy, dW, None)
+
+    for f in (dispatch, combine, grad):
+        assert f(t=3, T=-1) == TYPE and f(t=-1) == TYPE
+        for kw in (dict(T=-1), dict(k=-1), dict(H=-1), dict(rows=-1)):
+            assert f(**kw) == DIM
+        assert f(T=0) == OK
+        assert f(slot=None) == NULL and f(ldy=7) == LD
+        assert f(slot=FAKE + 2) == ALIGN and f(Y=FAKE + 1) == ALIGN and f(Y=FAKE + 2, t=0) == ALIGN
+        assert f(T=1 << 31) == UNSUP and f(T=1 << 30, k=2) == UNSUP and f(rows=1 << 31) == UNSUP
+    assert dispatch(rows=0, Y=None) == OK and dispatch(H=0) == OK
+    assert dispatch(X=None) == NULL and dispatch(Y=None) == NULL and dispatch(ldx=7) == LD
+    assert combine(O=None) == NULL and combine(Y=None) == NULL and combine(ldo=7) == LD
+    assert combine(w=FAKE + 1) == ALIGN and combine(O=FAKE + 1) == ALIGN
+    assert grad(dY=None, dW=None) == OK and grad(dO=None) == NULL and grad(Y=None) == NULL
+    assert grad(ldo=7) == LD and grad(lddy=7) == LD
+    assert grad(dO=FAKE + 1) == ALIGN and grad(dY=FAKE + 1) == ALIGN and grad(dW=FAKE + 2) == ALIGN
+    assert grad(w=FAKE + 2) == ALIGN
+
+
+def test_strerror_names_the_type_error(lib):
+    assert b"type" in lib.gemm_strerror(8)
+
+
+def test_python_functions_want_device_tensors():
+    import dense_gemm_02_amd as L
+    q = torch.zeros((4, 16), dtype=torch.int8)
+    s = torch.ones(4)
+    ids = torch.zeros((4, 2), dtype=torch.int64)
+    slot = torch.zeros((4, 2), dtype=torch.int32)
+    x = torch.zeros((4, 16))
+    for call in (lambda: L.quantize_i8(x), lambda: L.matmul(q, q.t(), scale_a=s, scale_b=s),
+                 lambda: L.matmul_grouped(q, q[None], slot[0], s, s), lambda: L.expert_sort(ids, 4),
+                 lambda: L.expert_dispatch(x, slot), lambda: L.expert_combine(x, slot),
+                 lambda: L.expert_dispatch_grad(x, slot), lambda: L.expert_combine_grad(x, x, slot),
+                 lambda: L.matmul_experts(x, ids, s, q[None], s)):
+        with pytest.raises(TypeError):
+            call()
