@@ -10,6 +10,23 @@ constexpr int kMaxExperts = 1024;
 constexpr int64_t kMaxCount = 0x7fffffff;
 
 // ---- sort -------------------------------------------------------------------------
+//
+// A stable counting sort.  The pairs are cut into one contiguous chunk per
+// workgroup and that into one per wave; a pair's place is
+//   pairs of lower experts + pairs of its expert in earlier chunks (of
+//   workgroups, then waves) + those before it in its own wave's chunk.
+// Up to kChunk pairs one workgroup does it alone; beyond, a first launch
+// leaves every chunk's counts in the workspace and each workgroup of the
+// second sums the columns it needs (chunks x experts words from the L2, at
+// most kBlocks x 1024; no third launch for the prefix sums, no atomics across
+// workgroups, so the order never depends on timing).
+//
+// Latency bounds it: a step's pairs take a few microseconds of loads and
+// barriers, not bytes.
+
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+constexpr int kChunk = 2048;     // pairs per workgroup, until there are kBlocks of them
+constexpr int kBlocks = 256;     // one per CU
 
 struct SortArgs {
   const void* ids;
@@ -17,66 +34,142 @@ struct SortArgs {
   int32_t* slot;
   int32_t* pair;
   int32_t* token;
-  int64_t n;
-  int k;
-  int experts;
+  int32_t* counts;    // [blocks][experts], with more than one block
+  int64_t n, chunk;   // pairs in all and per workgroup
+  int k, experts, blocks;
 };
 
+// The chunk of a workgroup: a whole number of waves' 64-pair steps.
+inline int64_t sort_chunk(int64_t n) {
+  const int64_t c = (n + kBlocks - 1) / kBlocks;
+  return c <= kChunk ? kChunk : (c + kSortThreads - 1) / kSortThreads * kSortThreads;
+}
+
 template <class Id>
-__device__ __forceinline__ int expert_of(const SortArgs& a, int64_t i) {
-  if (i >= a.n) return -1;
+__device__ __forceinline__ int expert_of(const SortArgs& a, int64_t i, int64_t end) {
+  if (i >= end) return -1;
   const Id id = ((const Id*)a.ids)[i];
   return id >= 0 && id < (Id)a.experts ? (int)id : -1;
 }
 
-// One workgroup: counts, their prefix sums, then the pairs in order, 1024 at
-// a time; a pair's place among those of its expert is found wave by wave.
+// First launch: the experts' counts in each chunk.
 template <class Id>
-__global__ void __launch_bounds__(1024) sort_kernel(const SortArgs a) {
-  __shared__ int32_t base[kMaxExperts + 1];
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortArgs a) {
+  __shared__ int32_t count[kMaxExperts];
   const int tid = threadIdx.x;
-  for (int e = tid; e <= a.experts; e += 1024) base[e] = 0;
+  if (tid < a.experts) count[tid] = 0;
   __syncthreads();
-  for (int64_t i = tid; i < a.n; i += 1024) {
-    const int e = expert_of<Id>(a, i);
-    if (e >= 0) atomicAdd(&base[e], 1);
+  const int64_t i0 = blockIdx.x * a.chunk, end = i0 + a.chunk < a.n ? i0 + a.chunk : a.n;
+  for (int64_t i = i0 + tid; i < end; i += kSortThreads) {
+    const int e = expert_of<Id>(a, i, end);
+    if (e >= 0) atomicAdd(&count[e], 1);
   }
   __syncthreads();
-  if (tid == 0) {
-    int32_t sum = 0;
-    for (int e = 0; e <= a.experts; ++e) {
-      const int32_t c = base[e];
-      base[e] = sum;
-      a.offsets[e] = sum;
-      sum += c;
-    }
+  if (tid < a.experts) a.counts[(int64_t)blockIdx.x * a.experts + tid] = count[tid];
+}
+
+// The places of a chunk's pairs; workgroup 0 also stores the offsets.
+template <class Id>
+__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs a) {
+  __shared__ int32_t place[kSortWaves][kMaxExperts];   // counts of each wave's pairs, then their next places
+  __shared__ int32_t part[2][kSortThreads];
+  __shared__ int32_t wave_sum[kSortWaves];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int E = a.experts;
+  const int64_t i0 = blockIdx.x * a.chunk, end = i0 + a.chunk < a.n ? i0 + a.chunk : a.n;
+  const int64_t per = a.chunk / kSortWaves;            // pairs per wave
+  const int64_t w0 = i0 + wave * per, w1 = w0 + per < end ? w0 + per : end;
+
+  for (int e = lane; e < E; e += 64) place[wave][e] = 0;
+  // (A wave counts into its own row only.)
+  for (int64_t i = w0 + lane; i < w1; i += 64) {
+    const int e = expert_of<Id>(a, i, w1);
+    if (e >= 0) atomicAdd(&place[wave][e], 1);
   }
-  __syncthreads();
-  const int32_t kept = base[a.experts];
-  for (int64_t i0 = 0; i0 < a.n; i0 += 1024) {
-    const int64_t i = i0 + tid;
-    const int e = expert_of<Id>(a, i);
-    for (int w = 0; w < 16; ++w) {
-      if (w == tid >> 6) {
-        uint64_t same = __ballot(e >= 0);
-        for (int b = 1; b < kMaxExperts; b *= 2) {
-          const uint64_t m = __ballot((e & b) != 0);
-          same &= (e & b) != 0 ? m : ~m;
-        }
-        const int rank = __popcll(same & ((1ull << (tid & 63)) - 1ull));
-        int32_t at = -1;
-        if (e >= 0) at = base[e] + rank;
-        if (i < a.n) a.slot[i] = at;
-        if (e >= 0) {
-          a.pair[at] = (int32_t)i;
-          if (a.token != nullptr) a.token[at] = (int32_t)i / a.k;
-          if (rank == 0) base[e] += __popcll(same);
-        }
+  // Columns of the counts: thread (g, e) sums chunks g, g + G, ... of expert e.
+  const int width = E <= 64 ? 64 : (E <= 128 ? 128 : (E <= 256 ? 256 : (E <= 512 ? 512 : 1024)));
+  const int groups = kSortThreads / width, g = tid / width, ge = tid % width;
+  int32_t before = 0, all = 0;
+  if (a.blocks > 1) {
+    if (ge < E) {
+#pragma unroll 4
+      for (int b = g; b < a.blocks; b += groups) {
+        const int32_t c = a.counts[(int64_t)b * E + ge];
+        all += c;
+        before += b < (int)blockIdx.x ? c : 0;
       }
-      __syncthreads();
+    }
+    part[0][tid] = before;
+    part[1][tid] = all;
+  }
+  __syncthreads();
+  before = all = 0;
+  if (tid < E) {
+    if (a.blocks > 1) {
+      for (int q = 0; q < groups; ++q) {
+        before += part[0][q * width + tid];
+        all += part[1][q * width + tid];
+      }
+    } else {
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) all += place[w][tid];
     }
   }
-  for (int64_t n = kept + tid; n < a.n; n += 1024) {
+  // Pairs of lower experts: an exclusive sum over the threads.
+  int32_t sum = all;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int32_t o = __shfl_up(sum, d);
+    if (lane >= d) sum += o;
+  }
+  if (lane == 63) wave_sum[wave] = sum;
+  __syncthreads();
+  int32_t kept = 0, first = sum - all;
+#pragma unroll
+  for (int w = 0; w < kSortWaves; ++w) {
+    const int32_t s = wave_sum[w];
+    first += w < wave ? s : 0;
+    kept += s;
+  }
+  if (blockIdx.x == 0) {
+    if (tid < E) a.offsets[tid] = first;
+    if (tid == 0) a.offsets[E] = kept;
+  }
+  if (tid < E) {
+    int32_t at = first + before;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int32_t c = place[w][tid];
+      place[w][tid] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  // Each wave places its pairs in order, 64 at a time: a lane's rank is the
+  // number of lower lanes with its expert, found bit by bit of the expert.
+  int bits = 0;
+  while ((1 << bits) < E) ++bits;
+  for (int64_t j = w0; j < w1; j += 64) {
+    const int64_t i = j + lane;
+    const int e = expert_of<Id>(a, i, w1);
+    uint64_t same = __ballot(e >= 0);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t m = __ballot((e >> b) & 1);
+      same &= (e >> b) & 1 ? m : ~m;
+    }
+    const int rank = __popcll(same & ((1ull << lane) - 1ull));
+    int32_t at = -1;
+    if (e >= 0) at = place[wave][e] + rank;
+    if (i < w1) a.slot[i] = at;
+    if (e >= 0) {
+      a.pair[at] = (int32_t)i;
+      if (a.token != nullptr) a.token[at] = (int32_t)i / a.k;
+      if (rank == 0) place[wave][e] += __popcll(same);
+    }
+  }
+  // No pairs behind the last place (each workgroup its share).
+  for (int64_t n = (kept > i0 ? kept : i0) + tid; n < end; n += kSortThreads) {
     a.pair[n] = -1;
     if (a.token != nullptr) a.token[n] = -1;
   }
@@ -176,7 +269,8 @@ extern "C" {
 int64_t expert_sort_workspace(int64_t tokens, int64_t k, int64_t experts) {
   using namespace dg;
   if (tokens < 0 || k < 0 || experts < 0 || experts > kMaxExperts || too_many(tokens, k, 0)) return -1;
-  return 0;
+  const int64_t n = tokens * k, blocks = (n + sort_chunk(n) - 1) / sort_chunk(n);
+  return blocks > 1 ? 4 * blocks * experts : 0;
 }
 
 int expert_sort(int64_t tokens, int64_t k, int64_t experts, const void* ids, int id_bytes, int32_t* offsets,
@@ -196,9 +290,15 @@ int expert_sort(int64_t tokens, int64_t k, int64_t experts, const void* ids, int
       !aligned_to(token, 4) ||
       (need > 0 && !aligned_to(workspace, 4)))
     return DGEMM_ERR_MISALIGNED;
-  SortArgs a{ids, offsets, slot, pair, token, n, (int)k, (int)experts};
-  const void* fn = id_bytes == 8 ? (const void*)&sort_kernel<int64_t> : (const void*)&sort_kernel<int32_t>;
-  return launch_kernel(fn, 1, 1024, &a, stream);
+  SortArgs a{ids, offsets, slot, pair, token, (int32_t*)workspace, n, sort_chunk(n), (int)k, (int)experts, 1};
+  if (n > a.chunk) a.blocks = (int)((n + a.chunk - 1) / a.chunk);
+  const bool wide = id_bytes == 8;
+  if (a.blocks > 1 && experts > 0) {
+    const void* fn = wide ? (const void*)&sort_count_kernel<int64_t> : (const void*)&sort_count_kernel<int32_t>;
+    if (const int st = launch_kernel(fn, a.blocks, kSortThreads, &a, stream)) return st;
+  }
+  const void* fn = wide ? (const void*)&sort_place_kernel<int64_t> : (const void*)&sort_place_kernel<int32_t>;
+  return launch_kernel(fn, a.blocks, kSortThreads, &a, stream);
 }
 
 int expert_dispatch(int64_t tokens, int64_t k, int64_t H, int type, const void* X, int64_t ldx, const int32_t* slot,
