@@ -18,4 +18,45 @@ auto with_type(int type, F f) {
   return f(__bf16{});
 }
 
+// Sixteen bytes of a row as FP32 values and back (rounded to nearest-even).
+template <class T>
+struct Pack {
+  static constexpr int N = 16 / (int)sizeof(T);
+  typedef T vec __attribute__((ext_vector_type(N)));
+  __device__ static void unpack(u32x4 v, float (&f)[N]) {
+    const vec t = __builtin_bit_cast(vec, v);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = (float)t[i];
+  }
+  __device__ static u32x4 pack(const float (&f)[N]) {
+    vec t;
+#pragma unroll
+    for (int i = 0; i < N; ++i) t[i] = (T)f[i];
+    return __builtin_bit_cast(u32x4, t);
+  }
+};
+
+// Elements h .. h + N - 1 of a row of H, zeros past its end.  V: the row is
+// 16-byte aligned and so is h (then one load where all of them are there).
+template <class T, bool V>
+__device__ __forceinline__ u32x4 load_pack(const T* row, int64_t h, int64_t H) {
+  if (V && h + Pack<T>::N <= H) return *(const u32x4*)(row + h);
+  typename Pack<T>::vec t;
+#pragma unroll
+  for (int i = 0; i < Pack<T>::N; ++i) t[i] = h + i < H ? row[h + i] : (T)0.0f;
+  return __builtin_bit_cast(u32x4, t);
+}
+
+template <class T, bool V>
+__device__ __forceinline__ void store_pack(T* row, int64_t h, int64_t H, u32x4 v) {
+  if (V && h + Pack<T>::N <= H) {
+    *(u32x4*)(row + h) = v;
+    return;
+  }
+  const typename Pack<T>::vec t = __builtin_bit_cast(typename Pack<T>::vec, v);
+#pragma unroll
+  for (int i = 0; i < Pack<T>::N; ++i)
+    if (h + i < H) row[h + i] = t[i];
+}
+
 }  // namespace dg

@@ -176,6 +176,19 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs
 }
 
 // ---- rows -------------------------------------------------------------------------
+//
+// All three move rows and little else: HBM bounds them.  WPT waves of a
+// workgroup of four take a token: all four where a row is longer than the
+// 1 KiB one wave covers, else one each.  (8191 tokens x 8 rows of 8 KiB,
+// combined: 123 us with four waves on a token, 176 with one, whose 8 x 1 KiB
+// pieces lie further apart; the floor of the bytes is 124 at the rate of a large
+// copy.)  A lane takes 16 bytes of the row at a time, of kBatch pairs at once,
+// so that kBatch loads per lane are in flight.  A token's slots are the same
+// for the whole wave and sit in scalar registers: a dropped pair costs a
+// branch and no traffic.
+
+constexpr int kBatch = 8;       // combine
+constexpr int kGradBatch = 4;   // combine_grad, which holds more per pair (8 parked scalars in vector registers)
 
 struct RowArgs {
   const void* x;      // rows by token, in
@@ -190,64 +203,156 @@ struct RowArgs {
   int64_t tokens, k, H, rows;
 };
 
-__device__ __forceinline__ int64_t slot_of(const RowArgs& a, int64_t pair) {
-  const int64_t s = a.slot[pair];
-  return s >= 0 && s < a.rows ? s : -1;
+// The token of this wave, -1 behind the last, and its part of the row.
+template <int WPT>
+__device__ __forceinline__ int64_t token_of(const RowArgs& a, int* part) {
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  *part = wave % WPT;
+  const int64_t t = (int64_t)blockIdx.x * (4 / WPT) + wave / WPT;
+  return t < a.tokens ? t : -1;
 }
 
-template <class T>
+// Slot of pair i, -1 if it is dropped.
+__device__ __forceinline__ int32_t slot_of(const RowArgs& a, int64_t i) {
+  const int32_t s = a.slot[i];
+  return (uint32_t)s < (uint32_t)a.rows ? s : -1;
+}
+
+template <class T, bool V, int WPT>
 __global__ void __launch_bounds__(256) dispatch_kernel(const RowArgs a) {
-  for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-    const T* x = (const T*)a.x + t * a.ldx;
+  using P = Pack<T>;
+  int part;
+  const int64_t t = token_of<WPT>(a, &part);
+  if (t < 0) return;
+  const T* x = (const T*)a.x + t * a.ldx;
+  for (int64_t h = (part * 64 + lane_id()) * P::N; h < a.H; h += WPT * 64 * P::N) {
+    const u32x4 v = load_pack<T, V>(x, h, a.H);
     for (int64_t j = 0; j < a.k; ++j) {
-      const int64_t s = slot_of(a, t * a.k + j);
-      if (s < 0) continue;
-      for (int64_t h = threadIdx.x; h < a.H; h += 256) ((T*)a.out)[s * a.ldo + h] = x[h];
+      const int32_t s = slot_of(a, t * a.k + j);
+      if (s >= 0) store_pack<T, V>((T*)a.out + s * a.ldo, h, a.H, v);
     }
   }
 }
 
-template <class T>
+template <class T, bool V, int WPT>
 __global__ void __launch_bounds__(256) combine_kernel(const RowArgs a) {
-  for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-    for (int64_t h = threadIdx.x; h < a.H; h += 256) {
-      float sum = 0.0f;
-      for (int64_t j = 0; j < a.k; ++j) {
-        const int64_t s = slot_of(a, t * a.k + j);
-        if (s < 0) continue;
-        const float y = (float)((const T*)a.y)[s * a.ldy + h];
-        sum = a.w != nullptr ? __builtin_fmaf(a.w[t * a.k + j], y, sum) : sum + y;
-      }
-      ((T*)a.out)[t * a.ldo + h] = (T)sum;
-    }
-  }
-}
-
-template <class T>
-__global__ void __launch_bounds__(256) combine_grad_kernel(const RowArgs a) {
-  __shared__ float part[4];
-  for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-    const T* d = (const T*)a.x + t * a.ldx;
-    for (int64_t j = 0; j < a.k; ++j) {
-      const int64_t s = slot_of(a, t * a.k + j);
-      const float w = a.w != nullptr ? a.w[t * a.k + j] : 1.0f;
-      float dot = 0.0f;
-      if (s >= 0) {
-        for (int64_t h = threadIdx.x; h < a.H; h += 256) {
-          const float g = (float)d[h];
-          if (a.dw != nullptr) dot = __builtin_fmaf(g, (float)((const T*)a.y)[s * a.ldy + h], dot);
-          if (a.out != nullptr) ((T*)a.out)[s * a.ldo + h] = (T)(w * g);
+  using P = Pack<T>;
+  int part;
+  const int64_t t = token_of<WPT>(a, &part);
+  if (t < 0) return;
+  for (int64_t h = (part * 64 + lane_id()) * P::N; h < a.H; h += WPT * 64 * P::N) {
+    float sum[P::N] = {};
+    for (int64_t j0 = 0; j0 < a.k; j0 += kBatch) {
+      u32x4 y[kBatch];
+      float w[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        // (A pair past the last, or dropped, adds 0 * 0.)
+        const int32_t s = j0 + j < a.k ? slot_of(a, t * a.k + j0 + j) : -1;
+        y[j] = u32x4{0, 0, 0, 0};
+        w[j] = 0.0f;
+        if (s >= 0) {
+          y[j] = load_pack<T, V>((const T*)a.y + s * a.ldy, h, a.H);
+          w[j] = a.w != nullptr ? a.w[t * a.k + j0 + j] : 1.0f;
         }
       }
-      if (a.dw == nullptr) continue;
 #pragma unroll
-      for (int o = 32; o > 0; o /= 2) dot += __shfl_xor(dot, o);
-      __syncthreads();
-      if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
-      __syncthreads();
-      if (threadIdx.x == 0) a.dw[t * a.k + j] = (part[0] + part[1]) + (part[2] + part[3]);
+      for (int j = 0; j < kBatch; ++j) {
+        float f[P::N];
+        P::unpack(y[j], f);
+#pragma unroll
+        for (int i = 0; i < P::N; ++i) sum[i] = __builtin_fmaf(w[j], f[i], sum[i]);
+      }
     }
+    store_pack<T, V>((T*)a.out + t * a.ldo, h, a.H, P::pack(sum));
   }
+}
+
+template <class T, bool V, int WPT>
+__global__ void __launch_bounds__(256) combine_grad_kernel(const RowArgs a) {
+  using P = Pack<T>;
+  __shared__ float sums[4][kGradBatch];
+  int part;
+  const int64_t t = token_of<WPT>(a, &part);
+  if (WPT == 1 && t < 0) return;   // (WPT 4: every workgroup has a token)
+  const T* x = (const T*)a.x + t * a.ldx;
+  for (int64_t j0 = 0; j0 < a.k; j0 += kGradBatch) {
+    int32_t s[kGradBatch];
+    float w[kGradBatch], dot[kGradBatch];
+#pragma unroll
+    for (int j = 0; j < kGradBatch; ++j) {
+      s[j] = j0 + j < a.k ? slot_of(a, t * a.k + j0 + j) : -1;
+      w[j] = s[j] >= 0 && a.w != nullptr ? a.w[t * a.k + j0 + j] : 1.0f;
+      dot[j] = 0.0f;
+    }
+    for (int64_t h = (part * 64 + lane_id()) * P::N; h < a.H; h += WPT * 64 * P::N) {
+      float d[P::N];
+      P::unpack(load_pack<T, V>(x, h, a.H), d);
+      u32x4 y[kGradBatch];
+#pragma unroll
+      for (int j = 0; j < kGradBatch; ++j)
+        if (s[j] >= 0 && a.dw != nullptr) y[j] = load_pack<T, V>((const T*)a.y + s[j] * a.ldy, h, a.H);
+#pragma unroll
+      for (int j = 0; j < kGradBatch; ++j) {
+        if (s[j] < 0) continue;
+        if (a.out != nullptr) {
+          float g[P::N];
+#pragma unroll
+          for (int i = 0; i < P::N; ++i) g[i] = w[j] * d[i];
+          store_pack<T, V>((T*)a.out + s[j] * a.ldo, h, a.H, P::pack(g));
+        }
+        if (a.dw != nullptr) {
+          float f[P::N];
+          P::unpack(y[j], f);
+#pragma unroll
+          for (int i = 0; i < P::N; ++i) dot[j] = __builtin_fmaf(d[i], f[i], dot[j]);
+        }
+      }
+    }
+    if (a.dw == nullptr) continue;
+    float mine = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kGradBatch; ++j) {
+#pragma unroll
+      for (int o = 32; o > 0; o /= 2) dot[j] += __shfl_xor(dot[j], o);
+      mine = lane_id() == j ? dot[j] : mine;
+    }
+    if constexpr (WPT > 1) {
+      __syncthreads();
+      if (lane_id() < kGradBatch) sums[part][lane_id()] = mine;
+      __syncthreads();
+      if (lane_id() < kGradBatch)
+        mine = (sums[0][lane_id()] + sums[1][lane_id()]) + (sums[2][lane_id()] + sums[3][lane_id()]);
+    }
+    if (part == 0 && lane_id() < kGradBatch && j0 + lane_id() < a.k) a.dw[t * a.k + j0 + lane_id()] = mine;
+  }
+}
+
+// A row operator's launch: the kernel for the type, the rows' alignment and
+// their length.
+enum RowOp { kDispatch, kCombine, kCombineGrad };
+
+template <class T, bool V, int WPT>
+const void* row_kernel(RowOp op) {
+  if (op == kDispatch) return (const void*)&dispatch_kernel<T, V, WPT>;
+  if (op == kCombine) return (const void*)&combine_kernel<T, V, WPT>;
+  return (const void*)&combine_grad_kernel<T, V, WPT>;
+}
+
+int launch_rows(RowOp op, int type, RowArgs a, void* stream) {
+  const int64_t e = type_bytes(type);
+  bool vec = true;
+  for (const void* p : {a.x, a.y, (const void*)a.out}) vec = vec && aligned_to(p, 16);
+  if (a.x != nullptr) vec = vec && a.ldx * e % 16 == 0;
+  if (a.y != nullptr) vec = vec && a.ldy * e % 16 == 0;
+  if (a.out != nullptr) vec = vec && a.ldo * e % 16 == 0;
+  const bool one = (a.H * e + 15) / 16 <= 64;   // one wave's width
+  const void* fn = with_type(type, [&](auto t) {
+    using T = decltype(t);
+    if (vec) return one ? row_kernel<T, true, 1>(op) : row_kernel<T, true, 4>(op);
+    return one ? row_kernel<T, false, 1>(op) : row_kernel<T, false, 4>(op);
+  });
+  return launch_kernel(fn, one ? (a.tokens + 3) / 4 : a.tokens, 256, &a, stream);
 }
 
 // The checks the three row operators share, up to the limits.
@@ -312,9 +417,7 @@ int expert_dispatch(int64_t tokens, int64_t k, int64_t H, int type, const void* 
   if (!aligned_to(X, e) || !aligned_to(Y, e) || !aligned_to(slot, 4)) return DGEMM_ERR_MISALIGNED;
   if (too_many(tokens, k, rows)) return DGEMM_ERR_UNSUPPORTED;
   RowArgs a{X, ldx, nullptr, 0, Y, ldy, slot, nullptr, nullptr, tokens, k, H, rows};
-  return with_type(type, [&](auto t) {
-    return launch_kernel((const void*)&dispatch_kernel<decltype(t)>, tokens, 256, &a, stream);
-  });
+  return launch_rows(kDispatch, type, a, stream);
 }
 
 int expert_combine(int64_t tokens, int64_t k, int64_t H, int type, const void* Y, int64_t rows, int64_t ldy,
@@ -330,9 +433,7 @@ int expert_combine(int64_t tokens, int64_t k, int64_t H, int type, const void* Y
     return DGEMM_ERR_MISALIGNED;
   if (too_many(tokens, k, rows)) return DGEMM_ERR_UNSUPPORTED;
   RowArgs a{nullptr, 0, Y, ldy, O, ldo, slot, weights, nullptr, tokens, k, H, rows};
-  return with_type(type, [&](auto t) {
-    return launch_kernel((const void*)&combine_kernel<decltype(t)>, tokens, 256, &a, stream);
-  });
+  return launch_rows(kCombine, type, a, stream);
 }
 
 int expert_combine_grad(int64_t tokens, int64_t k, int64_t H, int type, const void* dO, int64_t ldo, const void* Y,
@@ -350,9 +451,7 @@ int expert_combine_grad(int64_t tokens, int64_t k, int64_t H, int type, const vo
     return DGEMM_ERR_MISALIGNED;
   if (too_many(tokens, k, rows)) return DGEMM_ERR_UNSUPPORTED;
   RowArgs a{dO, ldo, Y, ldy, dY, lddy, slot, weights, dW, tokens, k, H, rows};
-  return with_type(type, [&](auto t) {
-    return launch_kernel((const void*)&combine_grad_kernel<decltype(t)>, tokens, 256, &a, stream);
-  });
+  return launch_rows(kCombineGrad, type, a, stream);
 }
 
 }  // extern "C"
