@@ -36,21 +36,30 @@ struct Pack {
   }
 };
 
-// Elements h .. h + N - 1 of a row of H, zeros past its end.  V: the row is
-// 16-byte aligned and so is h (then one load where all of them are there).
-template <class T, bool V>
+// How rows are accessed: element by element; 16 bytes at once (rows 16-byte
+// aligned, h a multiple of a pack); or that and past the caches (nontemporal),
+// for matrices larger than they are.
+enum RowAccess { kScalar = 0, kVector = 1, kStream = 2 };
+
+// Elements h .. h + N - 1 of a row of H, zeros past its end.  One 16-byte
+// access where all of them are there.
+template <class T, int A>
 __device__ __forceinline__ u32x4 load_pack(const T* row, int64_t h, int64_t H) {
-  if (V && h + Pack<T>::N <= H) return *(const u32x4*)(row + h);
+  if (A != kScalar && h + Pack<T>::N <= H) {
+    if constexpr (A == kStream) return __builtin_nontemporal_load((const u32x4*)(row + h));
+    else return *(const u32x4*)(row + h);
+  }
   typename Pack<T>::vec t;
 #pragma unroll
   for (int i = 0; i < Pack<T>::N; ++i) t[i] = h + i < H ? row[h + i] : (T)0.0f;
   return __builtin_bit_cast(u32x4, t);
 }
 
-template <class T, bool V>
+template <class T, int A>
 __device__ __forceinline__ void store_pack(T* row, int64_t h, int64_t H, u32x4 v) {
-  if (V && h + Pack<T>::N <= H) {
-    *(u32x4*)(row + h) = v;
+  if (A != kScalar && h + Pack<T>::N <= H) {
+    if constexpr (A == kStream) __builtin_nontemporal_store(v, (u32x4*)(row + h));
+    else *(u32x4*)(row + h) = v;
     return;
   }
   const typename Pack<T>::vec t = __builtin_bit_cast(typename Pack<T>::vec, v);

@@ -218,7 +218,7 @@ __device__ __forceinline__ int32_t slot_of(const RowArgs& a, int64_t i) {
   return (uint32_t)s < (uint32_t)a.rows ? s : -1;
 }
 
-template <class T, bool V, int WPT>
+template <class T, int V, int WPT>
 __global__ void __launch_bounds__(256) dispatch_kernel(const RowArgs a) {
   using P = Pack<T>;
   int part;
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const RowArgs a) {
   if (t < 0) return;
   const T* x = (const T*)a.x + t * a.ldx;
   for (int64_t h = (part * 64 + lane_id()) * P::N; h < a.H; h += WPT * 64 * P::N) {
-    const u32x4 v = load_pack<T, V>(x, h, a.H);
+    const u32x4 v = load_pack<T, V == kScalar ? kScalar : kVector>(x, h, a.H);
     for (int64_t j = 0; j < a.k; ++j) {
       const int32_t s = slot_of(a, t * a.k + j);
       if (s >= 0) store_pack<T, V>((T*)a.out + s * a.ldo, h, a.H, v);
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const RowArgs a) {
   }
 }
 
-template <class T, bool V, int WPT>
+template <class T, int V, int WPT>
 __global__ void __launch_bounds__(256) combine_kernel(const RowArgs a) {
   using P = Pack<T>;
   int part;
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const RowArgs a) {
   }
 }
 
-template <class T, bool V, int WPT>
+template <class T, int V, int WPT>
 __global__ void __launch_bounds__(256) combine_grad_kernel(const RowArgs a) {
   using P = Pack<T>;
   __shared__ float sums[4][kGradBatch];
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const RowArgs a) {
     }
     for (int64_t h = (part * 64 + lane_id()) * P::N; h < a.H; h += WPT * 64 * P::N) {
       float d[P::N];
-      P::unpack(load_pack<T, V>(x, h, a.H), d);
+      P::unpack(load_pack<T, V == kScalar ? kScalar : kVector>(x, h, a.H), d);
       u32x4 y[kGradBatch];
 #pragma unroll
       for (int j = 0; j < kGradBatch; ++j)
@@ -332,12 +332,17 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const RowArgs a) {
 // their length.
 enum RowOp { kDispatch, kCombine, kCombineGrad };
 
-template <class T, bool V, int WPT>
+template <class T, int V, int WPT>
 const void* row_kernel(RowOp op) {
   if (op == kDispatch) return (const void*)&dispatch_kernel<T, V, WPT>;
   if (op == kCombine) return (const void*)&combine_kernel<T, V, WPT>;
   return (const void*)&combine_grad_kernel<T, V, WPT>;
 }
+
+// Sorted rows of this many bytes and more go past the caches.  Dispatch, a copy
+// of its rows, combine (k = 8, rows of 8 KiB): 64 MiB 56 us through the
+// caches, 62 past them; 128 MiB 129 and 114; 256 MiB 247 and 229.
+constexpr int64_t kStreamBytes = 96ll << 20;
 
 int launch_rows(RowOp op, int type, RowArgs a, void* stream) {
   const int64_t e = type_bytes(type);
@@ -346,11 +351,13 @@ int launch_rows(RowOp op, int type, RowArgs a, void* stream) {
   if (a.x != nullptr) vec = vec && a.ldx * e % 16 == 0;
   if (a.y != nullptr) vec = vec && a.ldy * e % 16 == 0;
   if (a.out != nullptr) vec = vec && a.ldo * e % 16 == 0;
+  const bool stream_rows = a.tokens * a.k * a.H * e >= kStreamBytes;
   const bool one = (a.H * e + 15) / 16 <= 64;   // one wave's width
   const void* fn = with_type(type, [&](auto t) {
     using T = decltype(t);
-    if (vec) return one ? row_kernel<T, true, 1>(op) : row_kernel<T, true, 4>(op);
-    return one ? row_kernel<T, false, 1>(op) : row_kernel<T, false, 4>(op);
+    if (vec && stream_rows) return one ? row_kernel<T, kStream, 1>(op) : row_kernel<T, kStream, 4>(op);
+    if (vec) return one ? row_kernel<T, kVector, 1>(op) : row_kernel<T, kVector, 4>(op);
+    return one ? row_kernel<T, kScalar, 1>(op) : row_kernel<T, kScalar, 4>(op);
   });
   return launch_kernel(fn, one ? (a.tokens + 3) / 4 : a.tokens, 256, &a, stream);
 }
