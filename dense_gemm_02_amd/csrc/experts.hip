@@ -212,10 +212,13 @@ __device__ __forceinline__ int64_t token_of(const RowArgs& a, int* part) {
   return t < a.tokens ? t : -1;
 }
 
-// Slot of pair i, -1 if it is dropped.
-__device__ __forceinline__ int32_t slot_of(const RowArgs& a, int64_t i) {
-  const int32_t s = a.slot[i];
-  return (uint32_t)s < (uint32_t)a.rows ? s : -1;
+// Slots of pairs j0 .. of token t, all loaded at once; -1 past the last.
+template <int N>
+__device__ __forceinline__ void slots_of(const RowArgs& a, int64_t t, int64_t j0, int32_t (&s)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) s[j] = a.slot[t * a.k + (j0 + j < a.k ? j0 + j : a.k - 1)];
+#pragma unroll
+  for (int j = 0; j < N; ++j) s[j] = j0 + j < a.k && (uint32_t)s[j] < (uint32_t)a.rows ? s[j] : -1;
 }
 
 template <class T, int V, int WPT>
@@ -225,11 +228,14 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const RowArgs a) {
   const int64_t t = token_of<WPT>(a, &part);
   if (t < 0) return;
   const T* x = (const T*)a.x + t * a.ldx;
-  for (int64_t h = (part * 64 + lane_id()) * P::N; h < a.H; h += WPT * 64 * P::N) {
-    const u32x4 v = load_pack<T, V == kScalar ? kScalar : kVector>(x, h, a.H);
-    for (int64_t j = 0; j < a.k; ++j) {
-      const int32_t s = slot_of(a, t * a.k + j);
-      if (s >= 0) store_pack<T, V>((T*)a.out + s * a.ldo, h, a.H, v);
+  for (int64_t j0 = 0; j0 < a.k; j0 += kBatch) {
+    int32_t s[kBatch];
+    slots_of(a, t, j0, s);
+    for (int64_t h = (part * 64 + lane_id()) * P::N; h < a.H; h += WPT * 64 * P::N) {
+      const u32x4 v = load_pack<T, V == kScalar ? kScalar : kVector>(x, h, a.H);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (s[j] >= 0) store_pack<T, V>((T*)a.out + s[j] * a.ldo, h, a.H, v);
     }
   }
 }
@@ -240,21 +246,25 @@ __global__ void __launch_bounds__(256) combine_kernel(const RowArgs a) {
   int part;
   const int64_t t = token_of<WPT>(a, &part);
   if (t < 0) return;
+  // The first batch's slots and weights, and mostly the only one's, are kept.
+  int32_t s[kBatch];
+  float w[kBatch];
+  auto batch = [&](int64_t j0) {
+    slots_of(a, t, j0, s);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) w[j] = s[j] < 0 ? 0.0f : (a.w != nullptr ? a.w[t * a.k + j0 + j] : 1.0f);
+  };
+  if (a.k > 0) batch(0);
   for (int64_t h = (part * 64 + lane_id()) * P::N; h < a.H; h += WPT * 64 * P::N) {
     float sum[P::N] = {};
     for (int64_t j0 = 0; j0 < a.k; j0 += kBatch) {
+      if (a.k > kBatch) batch(j0);
       u32x4 y[kBatch];
-      float w[kBatch];
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         // (A pair past the last, or dropped, adds 0 * 0.)
-        const int32_t s = j0 + j < a.k ? slot_of(a, t * a.k + j0 + j) : -1;
         y[j] = u32x4{0, 0, 0, 0};
-        w[j] = 0.0f;
-        if (s >= 0) {
-          y[j] = load_pack<T, V>((const T*)a.y + s * a.ldy, h, a.H);
-          w[j] = a.w != nullptr ? a.w[t * a.k + j0 + j] : 1.0f;
-        }
+        if (s[j] >= 0) y[j] = load_pack<T, V>((const T*)a.y + s[j] * a.ldy, h, a.H);
       }
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
@@ -279,9 +289,9 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const RowArgs a) {
   for (int64_t j0 = 0; j0 < a.k; j0 += kGradBatch) {
     int32_t s[kGradBatch];
     float w[kGradBatch], dot[kGradBatch];
+    slots_of(a, t, j0, s);
 #pragma unroll
     for (int j = 0; j < kGradBatch; ++j) {
-      s[j] = j0 + j < a.k ? slot_of(a, t * a.k + j0 + j) : -1;
       w[j] = s[j] >= 0 && a.w != nullptr ? a.w[t * a.k + j0 + j] : 1.0f;
       dot[j] = 0.0f;
     }
