@@ -1,6 +1,8 @@
 // Row operators' shared pieces: element types and their conversions.
 #pragma once
 
+#include <type_traits>
+
 #include "common.hpp"
 #include "dgemm.h"
 
@@ -36,18 +38,24 @@ struct Pack {
   }
 };
 
-// How rows are accessed: element by element; 16 bytes at once (rows 16-byte
-// aligned, h a multiple of a pack); or that and past the caches (nontemporal),
-// for matrices larger than they are.
-enum RowAccess { kScalar = 0, kVector = 1, kStream = 2 };
+// Sixteen bytes at the alignment of T.  (gfx950 serves global accesses of any
+// alignment; 16-byte ones of aligned and unaligned rows are the same
+// instruction.)
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
+template <class T>
+struct Unaligned {
+  typedef std::conditional_t<sizeof(T) == 2, u32x4_at2, u32x4_at4> type;
+};
 
-// Elements h .. h + N - 1 of a row of H, zeros past its end.  One 16-byte
-// access where all of them are there.
-template <class T, int A>
+// Elements h .. h + N - 1 of a row of H, zeros past its end, in one access
+// where all of them are there.  STREAM: past the caches (nontemporal).
+template <class T, bool STREAM>
 __device__ __forceinline__ u32x4 load_pack(const T* row, int64_t h, int64_t H) {
-  if (A != kScalar && h + Pack<T>::N <= H) {
-    if constexpr (A == kStream) return __builtin_nontemporal_load((const u32x4*)(row + h));
-    else return *(const u32x4*)(row + h);
+  if (h + Pack<T>::N <= H) {
+    const typename Unaligned<T>::type* p = (const typename Unaligned<T>::type*)(row + h);
+    if constexpr (STREAM) return __builtin_nontemporal_load(p);
+    else return *p;
   }
   typename Pack<T>::vec t;
 #pragma unroll
@@ -55,11 +63,12 @@ __device__ __forceinline__ u32x4 load_pack(const T* row, int64_t h, int64_t H) {
   return __builtin_bit_cast(u32x4, t);
 }
 
-template <class T, int A>
+template <class T, bool STREAM>
 __device__ __forceinline__ void store_pack(T* row, int64_t h, int64_t H, u32x4 v) {
-  if (A != kScalar && h + Pack<T>::N <= H) {
-    if constexpr (A == kStream) __builtin_nontemporal_store(v, (u32x4*)(row + h));
-    else *(u32x4*)(row + h) = v;
+  if (h + Pack<T>::N <= H) {
+    typename Unaligned<T>::type* p = (typename Unaligned<T>::type*)(row + h);
+    if constexpr (STREAM) __builtin_nontemporal_store(v, p);
+    else *p = v;
     return;
   }
   const typename Pack<T>::vec t = __builtin_bit_cast(typename Pack<T>::vec, v);

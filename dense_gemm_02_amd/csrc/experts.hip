@@ -221,7 +221,7 @@ __device__ __forceinline__ void slots_of(const RowArgs& a, int64_t t, int64_t j0
   for (int j = 0; j < N; ++j) s[j] = j0 + j < a.k && (uint32_t)s[j] < (uint32_t)a.rows ? s[j] : -1;
 }
 
-template <class T, int V, int WPT>
+template <class T, bool STREAM, int WPT>
 __global__ void __launch_bounds__(256) dispatch_kernel(const RowArgs a) {
   using P = Pack<T>;
   int part;
@@ -232,15 +232,15 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const RowArgs a) {
     int32_t s[kBatch];
     slots_of(a, t, j0, s);
     for (int64_t h = (part * 64 + lane_id()) * P::N; h < a.H; h += WPT * 64 * P::N) {
-      const u32x4 v = load_pack<T, V == kScalar ? kScalar : kVector>(x, h, a.H);
+      const u32x4 v = load_pack<T, false>(x, h, a.H);
 #pragma unroll
       for (int j = 0; j < kBatch; ++j)
-        if (s[j] >= 0) store_pack<T, V>((T*)a.out + s[j] * a.ldo, h, a.H, v);
+        if (s[j] >= 0) store_pack<T, STREAM>((T*)a.out + s[j] * a.ldo, h, a.H, v);
     }
   }
 }
 
-template <class T, int V, int WPT>
+template <class T, bool STREAM, int WPT>
 __global__ void __launch_bounds__(256) combine_kernel(const RowArgs a) {
   using P = Pack<T>;
   int part;
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const RowArgs a) {
       for (int j = 0; j < kBatch; ++j) {
         // (A pair past the last, or dropped, adds 0 * 0.)
         y[j] = u32x4{0, 0, 0, 0};
-        if (s[j] >= 0) y[j] = load_pack<T, V>((const T*)a.y + s[j] * a.ldy, h, a.H);
+        if (s[j] >= 0) y[j] = load_pack<T, STREAM>((const T*)a.y + s[j] * a.ldy, h, a.H);
       }
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
@@ -274,11 +274,11 @@ __global__ void __launch_bounds__(256) combine_kernel(const RowArgs a) {
         for (int i = 0; i < P::N; ++i) sum[i] = __builtin_fmaf(w[j], f[i], sum[i]);
       }
     }
-    store_pack<T, V>((T*)a.out + t * a.ldo, h, a.H, P::pack(sum));
+    store_pack<T, STREAM>((T*)a.out + t * a.ldo, h, a.H, P::pack(sum));
   }
 }
 
-template <class T, int V, int WPT>
+template <class T, bool STREAM, int WPT>
 __global__ void __launch_bounds__(256) combine_grad_kernel(const RowArgs a) {
   using P = Pack<T>;
   __shared__ float sums[4][kGradBatch];
@@ -297,11 +297,11 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const RowArgs a) {
     }
     for (int64_t h = (part * 64 + lane_id()) * P::N; h < a.H; h += WPT * 64 * P::N) {
       float d[P::N];
-      P::unpack(load_pack<T, V == kScalar ? kScalar : kVector>(x, h, a.H), d);
+      P::unpack(load_pack<T, false>(x, h, a.H), d);
       u32x4 y[kGradBatch];
 #pragma unroll
       for (int j = 0; j < kGradBatch; ++j)
-        if (s[j] >= 0 && a.dw != nullptr) y[j] = load_pack<T, V>((const T*)a.y + s[j] * a.ldy, h, a.H);
+        if (s[j] >= 0 && a.dw != nullptr) y[j] = load_pack<T, STREAM>((const T*)a.y + s[j] * a.ldy, h, a.H);
 #pragma unroll
       for (int j = 0; j < kGradBatch; ++j) {
         if (s[j] < 0) continue;
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const RowArgs a) {
           float g[P::N];
 #pragma unroll
           for (int i = 0; i < P::N; ++i) g[i] = w[j] * d[i];
-          store_pack<T, V>((T*)a.out + s[j] * a.ldo, h, a.H, P::pack(g));
+          store_pack<T, STREAM>((T*)a.out + s[j] * a.ldo, h, a.H, P::pack(g));
         }
         if (a.dw != nullptr) {
           float f[P::N];
@@ -338,15 +338,15 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const RowArgs a) {
   }
 }
 
-// A row operator's launch: the kernel for the type, the rows' alignment and
-// their length.
+// A row operator's launch: the kernel for the type, the rows' length and how
+// many bytes they are.
 enum RowOp { kDispatch, kCombine, kCombineGrad };
 
-template <class T, int V, int WPT>
+template <class T, bool STREAM, int WPT>
 const void* row_kernel(RowOp op) {
-  if (op == kDispatch) return (const void*)&dispatch_kernel<T, V, WPT>;
-  if (op == kCombine) return (const void*)&combine_kernel<T, V, WPT>;
-  return (const void*)&combine_grad_kernel<T, V, WPT>;
+  if (op == kDispatch) return (const void*)&dispatch_kernel<T, STREAM, WPT>;
+  if (op == kCombine) return (const void*)&combine_kernel<T, STREAM, WPT>;
+  return (const void*)&combine_grad_kernel<T, STREAM, WPT>;
 }
 
 // Sorted rows of this many bytes and more go past the caches.  Dispatch, a copy
@@ -356,18 +356,12 @@ constexpr int64_t kStreamBytes = 96ll << 20;
 
 int launch_rows(RowOp op, int type, RowArgs a, void* stream) {
   const int64_t e = type_bytes(type);
-  bool vec = true;
-  for (const void* p : {a.x, a.y, (const void*)a.out}) vec = vec && aligned_to(p, 16);
-  if (a.x != nullptr) vec = vec && a.ldx * e % 16 == 0;
-  if (a.y != nullptr) vec = vec && a.ldy * e % 16 == 0;
-  if (a.out != nullptr) vec = vec && a.ldo * e % 16 == 0;
   const bool stream_rows = a.tokens * a.k * a.H * e >= kStreamBytes;
   const bool one = (a.H * e + 15) / 16 <= 64;   // one wave's width
   const void* fn = with_type(type, [&](auto t) {
     using T = decltype(t);
-    if (vec && stream_rows) return one ? row_kernel<T, kStream, 1>(op) : row_kernel<T, kStream, 4>(op);
-    if (vec) return one ? row_kernel<T, kVector, 1>(op) : row_kernel<T, kVector, 4>(op);
-    return one ? row_kernel<T, kScalar, 1>(op) : row_kernel<T, kScalar, 4>(op);
+    if (stream_rows) return one ? row_kernel<T, true, 1>(op) : row_kernel<T, true, 4>(op);
+    return one ? row_kernel<T, false, 1>(op) : row_kernel<T, false, 4>(op);
   });
   return launch_kernel(fn, one ? (a.tokens + 3) / 4 : a.tokens, 256, &a, stream);
 }

@@ -62,27 +62,120 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   return v;
 }
 
-template <class T>
-__global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
-  __shared__ uint32_t part[4];
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const T* x = (const T*)a.X + row * a.ldx;
-    int8_t* q = a.Q + row * a.ldq;
-    uint32_t m = 0;
-    for (int64_t k = threadIdx.x; k < a.K; k += 256) {
-      const uint32_t b = __builtin_bit_cast(uint32_t, (float)x[k]) & 0x7fffffffu;
-      m = b > m ? b : m;
-    }
-    m = wave_max(m);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
-    __syncthreads();
+// The maximum of a row over its WPR waves.
+template <int WPR>
+__device__ __forceinline__ uint32_t row_max(uint32_t m, uint32_t* part, int wave) {
+  m = wave_max(m);
+  if constexpr (WPR == 1) return m;
+  if (lane_id() == 0) part[wave] = m;
+  __syncthreads();
 #pragma unroll
-    for (int w = 0; w < 4; ++w) m = part[w] > m ? part[w] : m;
-    const RowScale r = row_scale(m);
-    if (threadIdx.x == 0) a.scale[row] = r.scale;
-    for (int64_t k = threadIdx.x; k < a.K; k += 256) q[k] = (int8_t)quantize_one((float)x[k], r);
+  for (int w = 0; w < WPR; ++w) m = part[w] > m ? part[w] : m;
+  return m;
+}
+
+template <int N>
+__device__ __forceinline__ uint32_t max_bits(const float (&f)[N], uint32_t m) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, f[i]) & 0x7fffffffu;
+    m = b > m ? b : m;
   }
+  return m;
+}
+
+// Quantised values of one pack to q[k ..].
+template <class T>
+__device__ __forceinline__ void store_quantized(int8_t* q, int64_t k, int64_t K, const float (&f)[Pack<T>::N],
+                                                const RowScale& r) {
+  constexpr int N = Pack<T>::N;
+  uint32_t d[N / 4];
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v |= ((uint32_t)quantize_one(f[4 * i + e], r) & 0xffu) << (8 * e);
+    d[i] = v;
+  }
+  if (k + N <= K) {
+    __builtin_memcpy(q + k, d, N);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (k + i < K) q[k + i] = (int8_t)(d[i / 4] >> (8 * (i % 4)));
+}
+
+// WPR waves of a workgroup of four take a row and hold all of it in
+// registers, NP packs of 16 bytes a lane: the row is read once.
+template <class T, int WPR, int NP>
+__global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
+  using P = Pack<T>;
+  __shared__ uint32_t part[4];
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int64_t row = (int64_t)blockIdx.x * (4 / WPR) + wave / WPR;
+  if (WPR < 4 && row >= a.rows) return;   // (WPR 4: every workgroup has a row)
+  const T* x = (const T*)a.X + row * a.ldx;
+  const int64_t k0 = (wave % WPR * 64 + lane_id()) * P::N;
+  u32x4 v[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) v[i] = load_pack<T, false>(x, k0 + i * (WPR * 64 * P::N), a.K);
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    float f[P::N];
+    P::unpack(v[i], f);
+    m = max_bits(f, m);
+  }
+  const RowScale r = row_scale(row_max<WPR>(m, part, wave));
+  if (wave % WPR == 0 && lane_id() == 0) a.scale[row] = r.scale;
+  int8_t* q = a.Q + row * a.ldq;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    float f[P::N];
+    P::unpack(v[i], f);
+    store_quantized<T>(q, k0 + i * (WPR * 64 * P::N), a.K, f, r);
+  }
+}
+
+// Rows longer than the registers hold: read twice (the second time mostly
+// from the caches), 1024 threads a row.
+template <class T>
+__global__ void __launch_bounds__(1024) quantize_long_kernel(const QuantArgs a) {
+  using P = Pack<T>;
+  __shared__ uint32_t part[16];
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int64_t row = blockIdx.x;
+  const T* x = (const T*)a.X + row * a.ldx;
+  uint32_t m = 0;
+  for (int64_t k = (int64_t)threadIdx.x * P::N; k < a.K; k += 1024 * P::N) {
+    float f[P::N];
+    P::unpack(load_pack<T, false>(x, k, a.K), f);
+    m = max_bits(f, m);
+  }
+  const RowScale r = row_scale(row_max<16>(m, part, wave));
+  if (threadIdx.x == 0) a.scale[row] = r.scale;
+  for (int64_t k = (int64_t)threadIdx.x * P::N; k < a.K; k += 1024 * P::N) {
+    float f[P::N];
+    P::unpack(load_pack<T, false>(x, k, a.K), f);
+    store_quantized<T>(a.Q + row * a.ldq, k, a.K, f, r);
+  }
+}
+
+// The kernel for rows of K elements and the rows per workgroup of 256 (0: the
+// long one, a row per workgroup of 1024): the fewest registers that hold the
+// row, a wave for up to two packs a lane.
+template <class T>
+const void* quantize_choice(int64_t K, int* rows) {
+  const int64_t packs = (K + Pack<T>::N - 1) / Pack<T>::N;
+  *rows = packs <= 128 ? 4 : (packs <= 256 * 8 ? 1 : 0);
+  if (packs <= 64) return (const void*)&quantize_kernel<T, 1, 1>;
+  if (packs <= 128) return (const void*)&quantize_kernel<T, 1, 2>;
+  if (packs <= 256) return (const void*)&quantize_kernel<T, 4, 1>;
+  if (packs <= 512) return (const void*)&quantize_kernel<T, 4, 2>;
+  if (packs <= 1024) return (const void*)&quantize_kernel<T, 4, 4>;
+  if (packs <= 2048) return (const void*)&quantize_kernel<T, 4, 8>;
+  return (const void*)&quantize_long_kernel<T>;
 }
 
 }  // namespace
@@ -99,7 +192,7 @@ extern "C" int quantize_i8(int64_t rows, int64_t K, const void* X, int64_t ldx, 
   if (!aligned_to(X, type_bytes(x_type)) || !aligned_to(scale, 4)) return DGEMM_ERR_MISALIGNED;
   if (rows > 0x7fffffff) return DGEMM_ERR_UNSUPPORTED;
   QuantArgs a{X, ldx, Q, ldq, scale, rows, K};
-  return with_type(x_type, [&](auto t) {
-    return launch_kernel((const void*)&quantize_kernel<decltype(t)>, rows, 256, &a, stream);
-  });
+  int per = 0;
+  const void* fn = with_type(x_type, [&](auto t) { return quantize_choice<decltype(t)>(K, &per); });
+  return launch_kernel(fn, per > 0 ? (rows + per - 1) / per : rows, per > 0 ? 256 : 1024, &a, stream);
 }
