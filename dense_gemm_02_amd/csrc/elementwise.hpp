@@ -12,6 +12,13 @@ inline int type_bytes(int type) { return type == DGEMM_F32 ? 4 : 2; }
 inline bool valid_type(int type) { return type >= DGEMM_F32 && type <= DGEMM_BF16; }
 inline bool aligned_to(const void* p, int64_t n) { return ((uintptr_t)p) % (uintptr_t)n == 0; }
 
+// Row matrices of this many bytes and more are read once and written past the
+// caches (nontemporal).  Measured on tokens dispatched to eight rows of 8 KiB
+// each, a copy of the rows, and combined: 64 MiB of rows 56 us through the
+// caches, 62 past them; 128 MiB 129 and 114; 256 MiB 247 and 229.  256 MiB
+// of rows quantised: 77 and 66.
+constexpr int64_t kStreamBytes = 96ll << 20;
+
 // f(T{}) with the element type of a dgemm_type.
 template <class F>
 auto with_type(int type, F f) {

@@ -349,11 +349,6 @@ const void* row_kernel(RowOp op) {
   return (const void*)&combine_grad_kernel<T, STREAM, WPT>;
 }
 
-// Sorted rows of this many bytes and more go past the caches.  Dispatch, a copy
-// of its rows, combine (k = 8, rows of 8 KiB): 64 MiB 56 us through the
-// caches, 62 past them; 128 MiB 129 and 114; 256 MiB 247 and 229.
-constexpr int64_t kStreamBytes = 96ll << 20;
-
 int launch_rows(RowOp op, int type, RowArgs a, void* stream) {
   const int64_t e = type_bytes(type);
   const bool stream_rows = a.tokens * a.k * a.H * e >= kStreamBytes;

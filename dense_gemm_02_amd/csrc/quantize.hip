@@ -6,6 +6,9 @@
 // can be off by one only next to the middle between two integers, and the
 // remainder x - n s (exact there: a multiple of the operands' last place that
 // is no larger than s) tells.
+//
+// HBM bounds it: e + 1 bytes an element, with about eight vector
+// instructions between (one for the maximum, seven to round, check and pack).
 #include "elementwise.hpp"
 #include "launch.hpp"
 
@@ -40,17 +43,40 @@ __device__ __forceinline__ RowScale row_scale(uint32_t max_bits) {
   return r;
 }
 
-__device__ __forceinline__ int quantize_one(float x, const RowScale& r) {
-  if (r.inv == 0.0f) return 0;
-  const float v = x * r.up;
-  float n = __builtin_rintf(v * r.inv);
-  const float rest = __builtin_fmaf(-n, r.s, v), half = 0.5f * r.s;
-  // Off the nearest integer, or on the middle but on the odd side.
-  const bool odd = ((int)n & 1) != 0;
-  if (rest > half || (rest == half && odd)) n += 1.0f;
-  else if (rest < -half || (rest == -half && odd)) n -= 1.0f;
-  n = n > 127.0f ? 127.0f : (n < -127.0f ? -127.0f : n);
-  return (int)n;
+// Integers near 0 in the last bits of a float: x + kMagic rounds x to the
+// nearest-even integer n, whose low byte is that of the sum.
+constexpr float kMagic = 0x1.8p23f;
+
+// Four values to four bytes.  Nearly always every |x - n s| is below s / 2
+// and n is right; else, and in rows so small that s is subnormal and a
+// quotient can pass 127, the lane goes through the values one by one.
+__device__ __forceinline__ uint32_t quantize4(const float* f, const RowScale& r) {
+  uint32_t t[4];
+  float worst = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float v = f[i], u = __builtin_fmaf(v, r.inv, kMagic);
+    const float rest = __builtin_fmaf(-(u - kMagic), r.s, v);
+    worst = __builtin_fmaxf(worst, __builtin_fabsf(rest));
+    t[i] = __builtin_bit_cast(uint32_t, u);
+  }
+  if (worst >= 0.5f * r.s || r.up != 1.0f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float v = f[i] * r.up;
+      float n = __builtin_rintf(v * r.inv);
+      const float rest = __builtin_fmaf(-n, r.s, v), half = 0.5f * r.s;
+      // Off the nearest integer, or on the middle but on the odd side.
+      const bool odd = ((int)n & 1) != 0;
+      if (rest > half || (rest == half && odd)) n += 1.0f;
+      else if (rest < -half || (rest == -half && odd)) n -= 1.0f;
+      t[i] = (uint32_t)(int)__builtin_fminf(__builtin_fmaxf(n, -127.0f), 127.0f);
+    }
+  }
+  // Low bytes of t[0 .. 3], in order.
+  const uint32_t lo = __builtin_amdgcn_perm(t[1], t[0], 0x0c0c0400u);
+  const uint32_t hi = __builtin_amdgcn_perm(t[3], t[2], 0x0c0c0400u);
+  return lo | hi << 16;
 }
 
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
@@ -74,14 +100,35 @@ __device__ __forceinline__ uint32_t row_max(uint32_t m, uint32_t* part, int wave
   return m;
 }
 
-template <int N>
-__device__ __forceinline__ uint32_t max_bits(const float (&f)[N], uint32_t m) {
+// The running maximum of |x| over packs: of the bits of 16-bit values two at
+// a time, or of FP32 values, ordered as their magnitudes in either case (NaN
+// highest).
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+template <class T>
+__device__ __forceinline__ uint32_t max_pack(u32x4 v, uint32_t m) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const uint32_t b = __builtin_bit_cast(uint32_t, f[i]) & 0x7fffffffu;
-    m = b > m ? b : m;
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      const u16x2 b = __builtin_bit_cast(u16x2, v[i] & 0x7fff7fffu);
+      m = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m), b));
+    } else {
+      const uint32_t b = v[i] & 0x7fffffffu;
+      m = b > m ? b : m;
+    }
   }
   return m;
+}
+
+// ... as the bits of one FP32 value.
+template <class T>
+__device__ __forceinline__ uint32_t max_value(uint32_t m) {
+  if constexpr (sizeof(T) == 4) {
+    return m;
+  } else {
+    const uint16_t b = (uint16_t)((m & 0xffffu) > (m >> 16) ? m & 0xffffu : m >> 16);
+    return __builtin_bit_cast(uint32_t, (float)__builtin_bit_cast(T, b));
+  }
 }
 
 // Quantised values of one pack to q[k ..].
@@ -91,12 +138,7 @@ __device__ __forceinline__ void store_quantized(int8_t* q, int64_t k, int64_t K,
   constexpr int N = Pack<T>::N;
   uint32_t d[N / 4];
 #pragma unroll
-  for (int i = 0; i < N / 4; ++i) {
-    uint32_t v = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v |= ((uint32_t)quantize_one(f[4 * i + e], r) & 0xffu) << (8 * e);
-    d[i] = v;
-  }
+  for (int i = 0; i < N / 4; ++i) d[i] = r.inv == 0.0f ? 0u : quantize4(f + 4 * i, r);
   if (k + N <= K) {
     __builtin_memcpy(q + k, d, N);
     return;
@@ -108,7 +150,7 @@ __device__ __forceinline__ void store_quantized(int8_t* q, int64_t k, int64_t K,
 
 // WPR waves of a workgroup of four take a row and hold all of it in
 // registers, NP packs of 16 bytes a lane: the row is read once.
-template <class T, int WPR, int NP>
+template <class T, bool STREAM, int WPR, int NP>
 __global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
   using P = Pack<T>;
   __shared__ uint32_t part[4];
@@ -119,15 +161,11 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
   const int64_t k0 = (wave % WPR * 64 + lane_id()) * P::N;
   u32x4 v[NP];
 #pragma unroll
-  for (int i = 0; i < NP; ++i) v[i] = load_pack<T, false>(x, k0 + i * (WPR * 64 * P::N), a.K);
+  for (int i = 0; i < NP; ++i) v[i] = load_pack<T, STREAM>(x, k0 + i * (WPR * 64 * P::N), a.K);
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    float f[P::N];
-    P::unpack(v[i], f);
-    m = max_bits(f, m);
-  }
-  const RowScale r = row_scale(row_max<WPR>(m, part, wave));
+  for (int i = 0; i < NP; ++i) m = max_pack<T>(v[i], m);
+  const RowScale r = row_scale(row_max<WPR>(max_value<T>(m), part, wave));
   if (wave % WPR == 0 && lane_id() == 0) a.scale[row] = r.scale;
   int8_t* q = a.Q + row * a.ldq;
 #pragma unroll
@@ -148,12 +186,9 @@ __global__ void __launch_bounds__(1024) quantize_long_kernel(const QuantArgs a) 
   const int64_t row = blockIdx.x;
   const T* x = (const T*)a.X + row * a.ldx;
   uint32_t m = 0;
-  for (int64_t k = (int64_t)threadIdx.x * P::N; k < a.K; k += 1024 * P::N) {
-    float f[P::N];
-    P::unpack(load_pack<T, false>(x, k, a.K), f);
-    m = max_bits(f, m);
-  }
-  const RowScale r = row_scale(row_max<16>(m, part, wave));
+  for (int64_t k = (int64_t)threadIdx.x * P::N; k < a.K; k += 1024 * P::N)
+    m = max_pack<T>(load_pack<T, false>(x, k, a.K), m);
+  const RowScale r = row_scale(row_max<16>(max_value<T>(m), part, wave));
   if (threadIdx.x == 0) a.scale[row] = r.scale;
   for (int64_t k = (int64_t)threadIdx.x * P::N; k < a.K; k += 1024 * P::N) {
     float f[P::N];
@@ -165,16 +200,16 @@ __global__ void __launch_bounds__(1024) quantize_long_kernel(const QuantArgs a) 
 // The kernel for rows of K elements and the rows per workgroup of 256 (0: the
 // long one, a row per workgroup of 1024): the fewest registers that hold the
 // row, a wave for up to two packs a lane.
-template <class T>
+template <class T, bool STREAM>
 const void* quantize_choice(int64_t K, int* rows) {
   const int64_t packs = (K + Pack<T>::N - 1) / Pack<T>::N;
   *rows = packs <= 128 ? 4 : (packs <= 256 * 8 ? 1 : 0);
-  if (packs <= 64) return (const void*)&quantize_kernel<T, 1, 1>;
-  if (packs <= 128) return (const void*)&quantize_kernel<T, 1, 2>;
-  if (packs <= 256) return (const void*)&quantize_kernel<T, 4, 1>;
-  if (packs <= 512) return (const void*)&quantize_kernel<T, 4, 2>;
-  if (packs <= 1024) return (const void*)&quantize_kernel<T, 4, 4>;
-  if (packs <= 2048) return (const void*)&quantize_kernel<T, 4, 8>;
+  if (packs <= 64) return (const void*)&quantize_kernel<T, STREAM, 1, 1>;
+  if (packs <= 128) return (const void*)&quantize_kernel<T, STREAM, 1, 2>;
+  if (packs <= 256) return (const void*)&quantize_kernel<T, STREAM, 4, 1>;
+  if (packs <= 512) return (const void*)&quantize_kernel<T, STREAM, 4, 2>;
+  if (packs <= 1024) return (const void*)&quantize_kernel<T, STREAM, 4, 4>;
+  if (packs <= 2048) return (const void*)&quantize_kernel<T, STREAM, 4, 8>;
   return (const void*)&quantize_long_kernel<T>;
 }
 
@@ -193,6 +228,10 @@ extern "C" int quantize_i8(int64_t rows, int64_t K, const void* X, int64_t ldx, 
   if (rows > 0x7fffffff) return DGEMM_ERR_UNSUPPORTED;
   QuantArgs a{X, ldx, Q, ldq, scale, rows, K};
   int per = 0;
-  const void* fn = with_type(x_type, [&](auto t) { return quantize_choice<decltype(t)>(K, &per); });
+  const bool stream_rows = rows * K * type_bytes(x_type) >= kStreamBytes;
+  const void* fn = with_type(x_type, [&](auto t) {
+    using T = decltype(t);
+    return stream_rows ? quantize_choice<T, true>(K, &per) : quantize_choice<T, false>(K, &per);
+  });
   return launch_kernel(fn, per > 0 ? (rows + per - 1) / per : rows, per > 0 ? 256 : 1024, &a, stream);
 }
