@@ -351,7 +351,7 @@ const void* row_kernel(RowOp op) {
 
 int launch_rows(RowOp op, int type, RowArgs a, void* stream) {
   const int64_t e = type_bytes(type);
-  const bool stream_rows = a.tokens * a.k * a.H * e >= kStreamBytes;
+  const bool stream_rows = a.tokens * a.k * a.H >= kStreamBytes / e;
   const bool one = (a.H * e + 15) / 16 <= 64;   // one wave's width
   const void* fn = with_type(type, [&](auto t) {
     using T = decltype(t);
@@ -368,8 +368,8 @@ int check_rows(int64_t tokens, int64_t k, int64_t H, int64_t rows, int type) {
   return DGEMM_OK;
 }
 
-bool too_many(int64_t tokens, int64_t k, int64_t rows) {
-  return tokens > kMaxCount || k > kMaxCount || tokens * k > kMaxCount || rows > kMaxCount;
+bool too_many(int64_t tokens, int64_t k, int64_t rows, int64_t H = 0) {
+  return tokens > kMaxCount || k > kMaxCount || tokens * k > kMaxCount || rows > kMaxCount || H > kMaxCount;
 }
 
 }  // namespace
@@ -421,7 +421,7 @@ int expert_dispatch(int64_t tokens, int64_t k, int64_t H, int type, const void* 
   if (ldx < H || ldy < H) return DGEMM_ERR_INVALID_LD;
   const int e = type_bytes(type);
   if (!aligned_to(X, e) || !aligned_to(Y, e) || !aligned_to(slot, 4)) return DGEMM_ERR_MISALIGNED;
-  if (too_many(tokens, k, rows)) return DGEMM_ERR_UNSUPPORTED;
+  if (too_many(tokens, k, rows, H)) return DGEMM_ERR_UNSUPPORTED;
   RowArgs a{X, ldx, nullptr, 0, Y, ldy, slot, nullptr, nullptr, tokens, k, H, rows};
   return launch_rows(kDispatch, type, a, stream);
 }
@@ -437,7 +437,7 @@ int expert_combine(int64_t tokens, int64_t k, int64_t H, int type, const void* Y
   const int e = type_bytes(type);
   if (!aligned_to(Y, e) || !aligned_to(O, e) || !aligned_to(slot, 4) || !aligned_to(weights, 4))
     return DGEMM_ERR_MISALIGNED;
-  if (too_many(tokens, k, rows)) return DGEMM_ERR_UNSUPPORTED;
+  if (too_many(tokens, k, rows, H)) return DGEMM_ERR_UNSUPPORTED;
   RowArgs a{nullptr, 0, Y, ldy, O, ldo, slot, weights, nullptr, tokens, k, H, rows};
   return launch_rows(kCombine, type, a, stream);
 }
@@ -455,7 +455,7 @@ int expert_combine_grad(int64_t tokens, int64_t k, int64_t H, int type, const vo
   if (!aligned_to(dO, e) || !aligned_to(Y, e) || !aligned_to(dY, e) || !aligned_to(slot, 4) ||
       !aligned_to(weights, 4) || !aligned_to(dW, 4))
     return DGEMM_ERR_MISALIGNED;
-  if (too_many(tokens, k, rows)) return DGEMM_ERR_UNSUPPORTED;
+  if (too_many(tokens, k, rows, H)) return DGEMM_ERR_UNSUPPORTED;
   RowArgs a{dO, ldo, Y, ldy, dY, lddy, slot, weights, dW, tokens, k, H, rows};
   return launch_rows(kCombineGrad, type, a, stream);
 }

@@ -225,10 +225,10 @@ extern "C" int quantize_i8(int64_t rows, int64_t K, const void* X, int64_t ldx, 
   if ((K > 0 && (X == nullptr || Q == nullptr)) || scale == nullptr) return DGEMM_ERR_NULL_POINTER;
   if (ldx < K || ldq < K) return DGEMM_ERR_INVALID_LD;
   if (!aligned_to(X, type_bytes(x_type)) || !aligned_to(scale, 4)) return DGEMM_ERR_MISALIGNED;
-  if (rows > 0x7fffffff) return DGEMM_ERR_UNSUPPORTED;
+  if (rows > 0x7fffffff || K > 0x7fffffff) return DGEMM_ERR_UNSUPPORTED;
   QuantArgs a{X, ldx, Q, ldq, scale, rows, K};
   int per = 0;
-  const bool stream_rows = rows * K * type_bytes(x_type) >= kStreamBytes;
+  const bool stream_rows = rows * K >= kStreamBytes / type_bytes(x_type);
   const void* fn = with_type(x_type, [&](auto t) {
     using T = decltype(t);
     return stream_rows ? quantize_choice<T, true>(K, &per) : quantize_choice<T, false>(K, &per);

@@ -184,10 +184,10 @@ int gemm_i8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda
  * DGEMM_ERR_INVALID_DIM; groups, N or groups*N above 2^31 - 1 ->
  * DGEMM_ERR_UNSUPPORTED; factor counts, rows_a against rows ->
  * DGEMM_ERR_INVALID_DIM; rows == 0, N == 0 or groups == 0 -> DGEMM_OK with no
- * work; NULL pointers (A and B may be NULL if K == 0, A and
- * scale_a if rows_a == 0); leading dimensions;
- * alignment; limits -> DGEMM_ERR_UNSUPPORTED: K above 131071; 256*lda, 256*ldb,
- * 4*rows, 4*rows_a, 4*N or (with row_index) rows_a*lda at or above 2^31.
+ * work; NULL pointers (A and B may be NULL if K == 0, A and scale_a if
+ * rows_a == 0); leading dimensions; alignment; limits ->
+ * DGEMM_ERR_UNSUPPORTED: K above 131071; 256*lda, 256*ldb, 4*rows, 4*rows_a,
+ * 4*N or (with row_index) rows_a*lda at or above 2^31.
  */
 int gemm_i8_grouped(int64_t groups, int64_t rows, int64_t N, int64_t K, const int8_t* A, int64_t rows_a, int64_t lda,
                     const int32_t* row_index, const int8_t* B, int64_t ldb, int64_t group_b, void* C, int64_t ldc,
@@ -205,7 +205,7 @@ int gemm_i8_grouped(int64_t groups, int64_t rows, int64_t N, int64_t K, const in
  * beyond that of the elements; elements of Q past K in a row are left.
  * Checks: x_type; negative sizes -> DGEMM_ERR_INVALID_DIM; rows == 0 ->
  * DGEMM_OK; NULL pointers (X and Q may be NULL if K == 0); leading
- * dimensions; alignment; rows above 2^31 - 1 -> DGEMM_ERR_UNSUPPORTED.
+ * dimensions; alignment; rows or K above 2^31 - 1 -> DGEMM_ERR_UNSUPPORTED.
  */
 int quantize_i8(int64_t rows, int64_t K, const void* X, int64_t ldx, int x_type, int8_t* Q, int64_t ldq,
                 float* scale, void* stream);
@@ -246,7 +246,7 @@ int quantize_i8(int64_t rows, int64_t K, const void* X, int64_t ldx, int x_type,
  * no atomics are used.
  * Checks: type (id_bytes); negative sizes -> DGEMM_ERR_INVALID_DIM; nothing
  * to do -> DGEMM_OK; NULL pointers; leading dimensions; alignment; limits
- * (tokens*k or rows above 2^31 - 1 -> DGEMM_ERR_UNSUPPORTED).
+ * (tokens*k, rows or H above 2^31 - 1 -> DGEMM_ERR_UNSUPPORTED).
  */
 int64_t expert_sort_workspace(int64_t tokens, int64_t k, int64_t experts);
 int expert_sort(int64_t tokens, int64_t k, int64_t experts, const void* ids, int id_bytes, int32_t* offsets,

@@ -197,6 +197,21 @@ def test_product_tiles(layout, M, N, K, dtype):
     near(lib().matmul(a, b, scale_a=sa, scale_b=sb, out_dtype=dtype), exact(a, b, sa, sb))
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("many", [1, 15, 31, 33, 250, 8159, 8161, 8200])
+def test_product_few_rows(many, dtype):
+    """Few rows on either side of the product, each number of 16-row tiles and
+    its edges, K whole, inside a chunk, below a stage and over many."""
+    for few in (1, 15, 16, 17, 32, 33, 63, 64, 65, 100, 128):
+        for K in (1, 128, 500, 2048, 4240) if few in (1, 17, 64, 100) else (333,):
+            if many > 300 and few not in (1, 17, 64, 100):
+                continue
+            print(f"few {few} many {many} K={K} {dtype}", flush=True)
+            a, b, sa, sb = operands("tn", few, many, K, few + many + K, pad=K % 2)
+            near(lib().matmul(a, b, scale_a=sa, scale_b=sb, out_dtype=dtype), exact(a, b, sa, sb))
+            near(lib().matmul(b.t(), a.t(), scale_a=sb, scale_b=sa, out_dtype=dtype), exact(b.t(), a.t(), sb, sa))
+
+
 TILES_TN = ["256x256_w4", "128x128_w4", "128x128_w4_s4", "192x256_w4", "256x192_w4", "256x256_pp"]
 TILES_NN = ["256x256_w4", "256x128_w4", "256x192_w4"]
 

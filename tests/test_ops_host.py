@@ -40,7 +40,7 @@ def test_i8_scaled_refusals(lib):
     assert i8(lib, ldb=33) == ALIGN and i8(lib, C=FAKE + 2) == ALIGN and i8(lib, C=FAKE + 1, c=1) == ALIGN
     assert i8(lib, sa=FAKE + 2) == ALIGN and i8(lib, sb=FAKE + 1) == ALIGN
     assert i8(lib, K=131072, lda=131072, ldb=131072) == UNSUP
-    assert i8(lib, M=300, na=300, lda=1 << 24, ldc=300) == UNSUP
+    assert i8(lib, M=300, na=300, N=300, nb=300, lda=1 << 24, ldc=300) == UNSUP
 
 
 def test_i8_kernel_choice(lib):
