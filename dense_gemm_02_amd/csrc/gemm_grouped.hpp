@@ -39,81 +39,76 @@ __device__ __forceinline__ void group_rows(const GroupedArgs& A, int64_t e, int*
 }
 
 // Inclusive sum over the lanes of a wave.
-__device__ __forceinline__ int64_t wave_scan(int64_t v) {
+__device__ __forceinline__ int wave_scan(int v) {
   const int lane = lane_id();
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
-    const int64_t o = __shfl_up(v, d);
+    const int o = __shfl_up(v, d);
     if (lane >= d) v += o;
   }
   return v;
 }
 
-// A value of lane `src` in scalar registers.
-__device__ __forceinline__ int64_t lane_value(int64_t v, int src) {
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, src);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)v >> 32), src);
-  return (int64_t)((uint64_t)hi << 32 | lo);
-}
-
 // The tile of workgroup blockIdx.x: false if there is none, else *g holds the
 // arguments of its product (one tile, at most BP x BQ of it valid) and *gt its
-// row index.
+// row index.  (Tiles and rows are counted in 32 bits: the grid is below 2^31.)
 template <int BP, int BQ, int OE>
 __device__ __forceinline__ bool group_tile(const GroupedArgs& A, GemmArgs* g, Gather* gt) {
   const int lane = lane_id();
-  const int64_t tiles_p = A.g.tiles_p;
-  int64_t mtiles = 0;
-  for (int64_t e0 = 0; e0 < A.groups; e0 += 64) {
-    int lo, hi;
-    group_rows(A, e0 + lane, &lo, &hi);
-    mtiles += lane_value(wave_scan((hi - lo + BQ - 1) / BQ), 63);
-  }
-  const int64_t total = mtiles * tiles_p, pid = blockIdx.x;
+  const uint32_t tiles_p = (uint32_t)A.g.tiles_p;
+  const int groups = (int)A.groups;
+  // Lanes' groups e0 + lane: rows, tiles along q and their sum up to here.
+  // One load of the offsets serves both the total and the search where there
+  // are at most 64 groups.
+  int e0 = 0, lo, hi, end;
+  auto look = [&](int e, int before) {
+    e0 = e;
+    group_rows(A, e + lane, &lo, &hi);
+    end = before + wave_scan((hi - lo + BQ - 1) / BQ);
+    return __builtin_amdgcn_readlane(end, 63);
+  };
+  int mtiles = look(0, 0);
+  for (int e = 64; e < groups; e += 64) mtiles = look(e, mtiles);
+  const uint32_t total = (uint32_t)mtiles * tiles_p, pid = blockIdx.x;
   if (pid >= total) return false;
   // XCD spread over the tiles there are (see tile_map).
-  const int64_t per = total / kXcds, extra = total % kXcds;
-  const int64_t xcd = pid % kXcds, local = pid / kXcds;
-  const int64_t lid = (xcd < extra ? xcd * (per + 1) : extra * (per + 1) + (xcd - extra) * per) + local;
-  const int64_t m = lid / tiles_p;
-  int64_t before = 0;
-  for (int64_t e0 = 0; e0 < A.groups; e0 += 64) {
-    int lo, hi;
-    group_rows(A, e0 + lane, &lo, &hi);
-    const int64_t mine = (hi - lo + BQ - 1) / BQ;
-    const int64_t end = before + wave_scan(mine);
-    const uint64_t past = __ballot(end > m);
-    if (past == 0) {
-      before = lane_value(end, 63);
-      continue;
-    }
-    const int src = __builtin_ctzll(past);
-    const int64_t e = e0 + src;
-    const int64_t mt = lane_value(mine, src);
-    const int64_t in = lid - (lane_value(end, src) - mt) * tiles_p;   // tile within the group
-    const int64_t r0 = __builtin_amdgcn_readlane(lo, src), r1 = __builtin_amdgcn_readlane(hi, src);
-    const int64_t width = A.g.group * mt;
-    const int64_t grp = in / width, first = grp * A.g.group;
-    const int64_t gsz = tiles_p - first < A.g.group ? tiles_p - first : A.g.group;
-    const int64_t rest = in - grp * width;
-    const int64_t p0 = (first + rest % gsz) * BP, q0 = r0 + rest / gsz * BQ;
-    *g = A.g;
-    g->P += e * A.pstride + p0 * A.g.ldp;
-    g->C = (char*)A.g.C + (q0 * A.g.ldc + p0) * OE;
-    if (A.g.sp_row) g->sp += e * A.g.Pn + p0;
-    g->Pn = A.g.Pn - p0;
-    g->Qn = r1 - q0;
-    g->tiles_p = g->tiles_q = g->group = 1;
-    *gt = A.gt;
-    if (A.gt.index != nullptr) {
-      gt->index += q0;
-    } else {
-      g->Q += q0 * A.g.ldq;
-      if (A.g.sq_row) g->sq += q0;
-    }
-    return true;
+  const uint32_t per = total / kXcds, extra = total % kXcds;
+  const uint32_t xcd = pid % kXcds, local = pid / kXcds;
+  const uint32_t lid = (xcd < extra ? xcd * (per + 1) : extra * (per + 1) + (xcd - extra) * per) + local;
+  const int m = (int)(lid / tiles_p);
+  int before = 0;
+  if (groups > 64) {
+    before = look(0, 0);
+    while (before <= m) before = look(e0 + 64, before);   // (m < mtiles, so it ends)
   }
-  return false;
+  const int src = __builtin_amdgcn_readfirstlane(__builtin_ctzll(__ballot(end > m)));
+  const int e = e0 + src;
+  const int r0 = __builtin_amdgcn_readlane(lo, src), r1 = __builtin_amdgcn_readlane(hi, src);
+  const uint32_t mt = (uint32_t)((r1 - r0 + BQ - 1) / BQ);
+  const uint32_t in = lid - ((uint32_t)__builtin_amdgcn_readlane(end, src) - mt) * tiles_p;   // tile within the group
+  const uint32_t width = (uint32_t)A.g.group * mt;
+  const uint32_t grp = in / width, first = grp * (uint32_t)A.g.group;
+  const uint32_t gsz = tiles_p - first < (uint32_t)A.g.group ? tiles_p - first : (uint32_t)A.g.group;
+  const uint32_t rest = in - grp * width;
+  // (The divisions run in vector registers; brought back, everything derived
+  // from them is scalar, and the copies' descriptors need no per-lane loops.)
+  auto scalar = [](uint32_t v) { return (int64_t)__builtin_amdgcn_readfirstlane((int)v); };
+  const int64_t p0 = scalar(first + rest % gsz) * BP, q0 = r0 + scalar(rest / gsz) * BQ;
+  *g = A.g;
+  g->P += e * A.pstride + p0 * A.g.ldp;
+  g->C = (char*)A.g.C + (q0 * A.g.ldc + p0) * OE;
+  if (A.g.sp_row) g->sp += e * A.g.Pn + p0;
+  g->Pn = A.g.Pn - p0;
+  g->Qn = r1 - q0;
+  g->tiles_p = g->tiles_q = g->group = 1;
+  *gt = A.gt;
+  if (A.gt.index != nullptr) {
+    gt->index += q0;
+  } else {
+    g->Q += q0 * A.g.ldq;
+    if (A.g.sq_row) g->sq += q0;
+  }
+  return true;
 }
 
 }  // namespace dg

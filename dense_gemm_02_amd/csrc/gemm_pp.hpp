@@ -64,8 +64,9 @@ struct PpCfg {
 };
 
 // KT: K ends inside a stage, so the copies carry per-lane tail masks.
-template <class Op, bool KT, class TileOf>
-__device__ __forceinline__ void gemm_pp_body(const GemmArgs& a, TileOf tile_of) {
+// GA: row q of Q is row gt.index[q] of its storage.
+template <class Op, bool KT, class TileOf, bool GA = false>
+__device__ __forceinline__ void gemm_pp_body(const GemmArgs& a, TileOf tile_of, const Gather& gt = Gather{}) {
   using Cfg = PpCfg<Op>;
   constexpr int E = Cfg::E, FC = Cfg::FC, ROWB = Cfg::ROWB, BK = Cfg::BK, CPE = Cfg::CPE;
   constexpr int TP = Cfg::TP, TQ = Cfg::TQ, MT = Cfg::MT, CPK = Cfg::CPK, KSTEPS = Cfg::KSTEPS;
@@ -98,9 +99,9 @@ __device__ __forceinline__ void gemm_pp_body(const GemmArgs& a, TileOf tile_of) 
   const int64_t p0 = tp * Cfg::BP, q0 = tq * Cfg::BQ;
   const int64_t qrows = (a.Qn - q0) < Cfg::BQ ? (a.Qn - q0) : Cfg::BQ;
   const int64_t prows = (a.Pn - p0) < Cfg::BP ? (a.Pn - p0) : Cfg::BP;
-  const char* qsrc = a.Q + q0 * a.ldq;
+  const char* qsrc = GA ? a.Q : a.Q + q0 * a.ldq;
   const char* psrc = a.P + p0 * a.ldp;
-  const uint32_t qn = (uint32_t)((qrows - 1) * a.ldq) + kbytes16;
+  const uint32_t qn = (uint32_t)(((GA ? gt.rows : qrows) - 1) * a.ldq) + kbytes16;
   const uint32_t pn = (uint32_t)((prows - 1) * a.ldp) + kbytes16;
 
   // ---- copies: P rows by group 0, Q rows by group 1 ----
@@ -116,6 +117,13 @@ __device__ __forceinline__ void gemm_pp_body(const GemmArgs& a, TileOf tile_of) 
   const int64_t cld = grp == 0 ? a.ldp : a.ldq;
   const uint32_t cv0 = (uint32_t)((8 * simd + (lane >> 3)) * cld + dkc * 16);
   const uint32_t cstep = (uint32_t)(32 * cld);
+  [[maybe_unused]] uint32_t cvi[Cfg::QSEG];   // GA: offsets of the copies, one by one
+  if constexpr (GA) {
+#pragma unroll
+    for (int i = 0; i < Cfg::QSEG; ++i)
+      cvi[i] = grp == 0 ? cv0 + i * cstep
+                        : gather_row(gt, q0 + 8 * (i * Cfg::NSIMD + simd) + (lane >> 3), a.Qn, a.ldq, dkc * 16);
+  }
   auto p_slot = [&](int t) { return smem + (t & 1) * Cfg::P_LDS; };
   auto q_slot = [&](int t) { return smem + Cfg::Q_BASE + (t % 3) * Cfg::Q_LDS; };
   // Stage t of this wave's operand into its slot.
@@ -135,7 +143,7 @@ __device__ __forceinline__ void gemm_pp_body(const GemmArgs& a, TileOf tile_of) 
     for (int i = 0; i < Cfg::PSEG; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           r, (__attribute__((address_space(3))) void*)(sb + (i * Cfg::NSIMD + simd) * 1024), 16,
-          (cv0 + i * cstep) | kill, 0, 0, 0);
+          (GA ? cvi[i] : cv0 + i * cstep) | kill, 0, 0, 0);
   };
 
   // Any K (integers): the part of Q's chunks at and past K becomes zero once
@@ -235,9 +243,9 @@ __device__ __forceinline__ void gemm_pp_body(const GemmArgs& a, TileOf tile_of) 
 
   // Epilogue: every wave is past its last LDS read; each stages its own
   // 64 rows of C (64 x 256 bytes) through LDS.
-  staged_epilogue<Op, Cfg::WTP, Cfg::WTQ, TP, TQ, MT, typename Op::Acc16>(
+  staged_epilogue<Op, Cfg::WTP, Cfg::WTQ, TP, TQ, MT, typename Op::Acc16, GA>(
       a, smem + wave * (Cfg::WTQ * 256), acc, lane, p0 + wp * Cfg::WTP,
-      q0 + wq * (Cfg::BQ / 2) + grp * Cfg::WTQ);
+      q0 + wq * (Cfg::BQ / 2) + grp * Cfg::WTQ, gt);
   stamp(2);
 }
 

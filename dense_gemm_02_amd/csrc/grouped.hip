@@ -1,36 +1,133 @@
 // gemm_i8_grouped: argument checks, kernel choice and launch.
+#include <math.h>
+#include <stdlib.h>
+#include <string.h>
+
 #include "dgemm.h"
 #include "gemm_grouped.hpp"
+#include "gemm_i8_skinny.hpp"
+#include "gemm_pp.hpp"
 #include "gemm_tn.hpp"
 #include "launch.hpp"
 
 namespace dg {
 namespace {
 
-// The four-wave kernel over the groups' tiles (K-tail masks in any case).
-template <class Op, int BP, int BQ, bool GA>
+// The block kernels and the skinny kernel over the groups' tiles.
+template <class Op, int BP, int BQ, bool KT, bool GA>
 __global__ void __launch_bounds__(256)
 __attribute__((amdgpu_waves_per_eu(TnCfg<Op, false, BP, BQ, 2>::WPE, TnCfg<Op, false, BP, BQ, 2>::WPE)))
 grouped_kernel(const GroupedArgs A) {
   GemmArgs g;
   Gather gt;
   if (!group_tile<BP, BQ, Op::OE>(A, &g, &gt)) return;
-  gemm_tn_body<Op, false, BP, BQ, 2, true, OneTile, GA>(g, OneTile{}, gt);
+  gemm_tn_body<Op, false, BP, BQ, 2, KT, OneTile, GA>(g, OneTile{}, gt);
 }
 
-template <class Op, int BP, int BQ>
-Launch four_wave(bool ga) {
+template <class Op, bool KT, bool GA>
+__global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
+grouped_pp(const GroupedArgs A) {
+  GemmArgs g;
+  Gather gt;
+  if (!group_tile<256, 256, Op::OE>(A, &g, &gt)) return;
+  gemm_pp_body<Op, KT, OneTile, GA>(g, OneTile{}, gt);
+}
+
+template <class Op, int SF, int FF, int D, bool GA>
+__global__ void __launch_bounds__(512) grouped_skinny(const GroupedArgs A) {
+  GemmArgs g;
+  Gather gt;
+  if (!group_tile<16 * SF, 16 * FF, Op::OE>(A, &g, &gt)) return;
+  gemm_i8_skinny_body<Op, SF, FF, 8, D, false, GA>(g, gt);
+}
+
+template <class Op, int BP, int BQ, bool GA>
+Launch four_wave(const char* name, bool kt) {
   using Cfg = TnCfg<Op, false, BP, BQ, 2>;
-  return Launch{ga ? (const void*)&grouped_kernel<Op, BP, BQ, true> : (const void*)&grouped_kernel<Op, BP, BQ, false>,
-                "i8_grouped", BP, BQ, Cfg::NT, Cfg::LDS, false};
+  return Launch{kt ? (const void*)&grouped_kernel<Op, BP, BQ, true, GA>
+                   : (const void*)&grouped_kernel<Op, BP, BQ, false, GA>,
+                name, BP, BQ, Cfg::NT, Cfg::LDS, false};
 }
 
-Launch select(int c_type, bool ga) {
-  switch (c_type) {
-    case DGEMM_F32: return four_wave<OpI8F, 128, 128>(ga);
-    case DGEMM_F16: return four_wave<OpI8H, 128, 128>(ga);
-    default: return four_wave<OpI8B, 128, 128>(ga);
+template <class Op, int SF, int FF, bool GA>
+Launch skinny(const char* name) {
+  using Cfg = SkinnyI8Cfg<SF, FF, 8, 1>;
+  return Launch{(const void*)&grouped_skinny<Op, SF, FF, 1, GA>, name, Cfg::SR, Cfg::FR, Cfg::NT, Cfg::LDS, false};
+}
+
+enum Kind { kPingPong, kFourWave, kSkinny16, kSkinny32, kSkinny64, kKinds };
+const char* const kNames[kKinds] = {"i8_grouped_256x256_pp", "i8_grouped_128x128_w4", "i8_grouped_skinny16",
+                                    "i8_grouped_skinny32", "i8_grouped_skinny64"};
+
+template <class Op, bool GA>
+Launch launch_of(int kind, bool kt) {
+  switch (kind) {
+    case kPingPong: {
+      using Cfg = PpCfg<Op>;
+      return Launch{kt ? (const void*)&grouped_pp<Op, true, GA> : (const void*)&grouped_pp<Op, false, GA>,
+                    kNames[kind], 256, 256, Cfg::NT, Cfg::LDS, false};
+    }
+    case kFourWave: return four_wave<Op, 128, 128, GA>(kNames[kind], kt);
+    case kSkinny16: return skinny<Op, 2, 1, GA>(kNames[kind]);
+    case kSkinny32: return skinny<Op, 2, 2, GA>(kNames[kind]);
+    default: return skinny<Op, 2, 4, GA>(kNames[kind]);
   }
+}
+
+template <bool GA>
+Launch launch_for(int c_type, int kind, bool kt) {
+  switch (c_type) {
+    case DGEMM_F32: return launch_of<OpI8F, GA>(kind, kt);
+    case DGEMM_F16: return launch_of<OpI8H, GA>(kind, kt);
+    default: return launch_of<OpI8B, GA>(kind, kt);
+  }
+}
+
+// The kernel for `rows` rows spread over `groups` groups, whose sizes only the
+// device knows: every group that can have rows is taken to have some, with a
+// part-filled last tile half the time.  Estimated time in us: the larger of
+// what the kernel's tiles cost and of what reading the groups' weights costs it,
+//   256 x 256 (ping-pong, one per CU)   a round 13 us and 10.25 ns per k; weights at 3.8 TB/s
+//   128 x 128 (four waves, two per CU)  a round 10 us and 7.7 ns per k; weights at 4.1 TB/s
+//   skinny                              40 GB/s per CU of (32 + few) rows; weights at 4.9 TB/s
+// Measured (us; 256 x 256 / 128 x 128 / skinny of 16 / of 32), rows read
+// through an index, sizes uneven as a router's:
+//   128 rows, 64 groups, N 2048, K 4096     99 /  83 /   56 /   64
+//   512                                    124 / 114 /   86 /   97
+//   2048                                   147 / 156 /  164 /  154
+//   8192                                   181 / 178 /  421 /  345
+//   512 rows, 8 groups, N 4096, K 14336    152 / 126 /  208 /  159
+//   2006                                   169 / 261 /  623 /  490
+//   4096                                   308 / 361 / 1228 /  970
+//   32768 rows, 32 groups, N 4096, K 4096  518 / 707 / 2802 / 2064
+int choose_kind(int64_t groups, int64_t rows, int64_t N, int64_t K) {
+  const double cus = 256.0;
+  const double some = (double)(groups < rows ? groups : rows);
+  const double weights = some * (double)N * (double)K;   // bytes
+  auto tiles = [&](int bq) {
+    const double t = (double)rows / bq + 0.5 * some;
+    return t > some ? t : some;
+  };
+  auto rounds = [&](int bp, int bq, int per_cu) {
+    return ceil(tiles(bq) * (double)((N + bp - 1) / bp) / (cus * per_cu));
+  };
+  auto larger = [](double x, double y) { return x > y ? x : y; };
+  double t[kKinds];
+  t[kPingPong] = larger(rounds(256, 256, 1) * (13.0 + (double)K * 10.25e-3), weights / 3.8e6);
+  t[kFourWave] = larger(rounds(128, 128, 2) * (10.0 + (double)K * 7.7e-3), weights / 4.1e6);
+  for (int kind = kSkinny16; kind <= kSkinny64; ++kind) {
+    const int few = 16 << (kind - kSkinny16);
+    const double wgs = tiles(few) * (double)((N + 31) / 32) / cus;
+    t[kind] = larger((wgs > 1 ? wgs : 1) * (32 + few) * (double)K / 40e3, weights / 4.9e6);
+  }
+  // (Sweeps and tests: DGEMM_CONFIG=<kernel name> forces a kernel, as for gemm_*.)
+  if (const char* want = getenv("DGEMM_CONFIG"))
+    for (int kind = 0; kind < kKinds; ++kind)
+      if (strcmp(want, kNames[kind]) == 0) return kind;
+  int best = 0;
+  for (int kind = 1; kind < kKinds; ++kind)
+    if (t[kind] < t[best]) best = kind;
+  return best;
 }
 
 constexpr int64_t kMaxCount = 0x7fffffff;
@@ -73,7 +170,9 @@ extern "C" int gemm_i8_grouped(int64_t groups, int64_t rows, int64_t N, int64_t 
   // An index over no rows: every row counts as zeros, as with K == 0.
   if (rows_a == 0) K = 0;
 
-  const Launch L = select(c_type, row_index != nullptr);
+  const int kind = choose_kind(groups, rows, N, K);
+  const bool kt = K % 128 != 0;
+  const Launch L = row_index != nullptr ? launch_for<true>(c_type, kind, kt) : launch_for<false>(c_type, kind, kt);
   GroupedArgs a{};
   GemmArgs& g = a.g;
   g.P = (const char*)B; g.ldp = ldb; g.Pn = N;

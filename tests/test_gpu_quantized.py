@@ -373,6 +373,26 @@ def test_grouped_larger(counts, N, K, gather):
     near(lib().matmul_grouped(*c[:5], out_dtype=torch.bfloat16, row_index=c[5]), grouped_exact(*c))
 
 
+@pytest.mark.parametrize("gather", [False, True], ids=["sorted", "gather"])
+@pytest.mark.parametrize("kernel", ["256x256_pp", "128x128_w4", "skinny16", "skinny32", "skinny64"])
+def test_grouped_every_kernel(monkeypatch, kernel, gather):
+    """Each kernel a grouped product can take, on groups below, at and past its
+    tile, K from below a stage to several, whole and ending inside a chunk."""
+    monkeypatch.setenv("DGEMM_CONFIG", "i8_grouped_" + kernel)
+    for i, (counts, N) in enumerate((([1, 0, 15, 16, 17, 0, 33], 70), ([257, 31, 128, 0, 64, 65], 300),
+                                     ([0, 300, 1], 513), ([3] * 70, 40))):
+        for K in (1, 100, 128, 256, 399, 1040):
+            for dtype in TYPES:
+                print(f"grouped {kernel} {counts[:6]} N={N} K={K} {dtype}", flush=True)
+                c = grouped_case(counts, N, K, 70 + i + K, gather, tail=3, lead=2)
+                got = torch.full((c[6], N), 7.0, device="cuda").to(dtype)
+                lib().matmul_grouped(*c[:5], out=got, row_index=c[5])
+                want = grouped_exact(*c)
+                written = ~torch.isnan(want[:, 0])
+                assert (got[~written] == 7).all()
+                near(got[written], want[written])
+
+
 def test_grouped_indexes_without_a_row():
     """Indexes outside a count as zeros with the factor 0; the same row many
     times; an a with no rows."""
