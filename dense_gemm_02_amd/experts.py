@@ -30,11 +30,14 @@ def expert_sort(ids, experts, with_token=False, stream=None):
         raise ValueError("ids must be contiguous, one row of choices for each token")
     T, k = ids.shape
     n = T * k
+    if not 0 <= experts < 2 ** 31:
+        raise ValueError("experts must be a count")
     # One allocation for all results.
     buf = torch.empty((experts + 1 + (3 if with_token else 2) * n,), dtype=torch.int32, device=device)
-    offsets, slot = buf[:experts + 1], buf[experts + 1:experts + 1 + n].view(T, k)
-    pair = buf[experts + 1 + n:experts + 1 + 2 * n]
-    token = buf[experts + 1 + 2 * n:] if with_token else None
+    at = experts + 1
+    offsets, slot = buf.as_strided((at,), (1,)), buf.as_strided((T, k), (k, 1), at)
+    pair = buf.as_strided((n,), (1,), at + n)
+    token = buf.as_strided((n,), (1,), at + 2 * n) if with_token else None
     need = load_library().expert_sort_workspace(T, k, experts)
     ws = None
     if need > 0:
@@ -80,8 +83,9 @@ def expert_dispatch(x, slot, out=None, rows=None, stream=None):
     H = x.shape[-1]
     ldx = _rows(x, "x", T, H, x.dtype)
     if out is None:
-        out = torch.empty((T * k if rows is None else rows, H), dtype=x.dtype, device=device)
-    ldy = _rows(out, "out", rows, H, x.dtype)
+        out, ldy = torch.empty((T * k if rows is None else rows, H), dtype=x.dtype, device=device), H
+    else:
+        ldy = _rows(out, "out", rows, H, x.dtype)
     call("expert_dispatch", device, stream, T, k, H, code, x.data_ptr(), ldx, slot.data_ptr(), out.data_ptr(),
          out.shape[0], ldy)
     return out
@@ -99,8 +103,9 @@ def expert_combine(y, slot, weights=None, out=None, stream=None):
     ldy = _rows(y, "y", None, H, y.dtype)
     w = _weights(weights, slot)
     if out is None:
-        out = torch.empty((T, H), dtype=y.dtype, device=device)
-    ldo = _rows(out, "out", T, H, y.dtype)
+        out, ldo = torch.empty((T, H), dtype=y.dtype, device=device), H
+    else:
+        ldo = _rows(out, "out", T, H, y.dtype)
     call("expert_combine", device, stream, T, k, H, code, y.data_ptr(), y.shape[0], ldy, slot.data_ptr(), w,
          out.data_ptr(), ldo)
     return out
@@ -126,11 +131,12 @@ def expert_combine_grad(dout, y, slot, weights=None, dy=None, dweights=None, str
     ldo = _rows(dout, "dout", T, H, y.dtype)
     w = _weights(weights, slot)
     if dy is None:
-        dy = torch.empty((y.shape[0], H), dtype=y.dtype, device=device)
-    lddy = _rows(dy, "dy", y.shape[0], H, y.dtype)
+        dy, lddy = torch.empty((y.shape[0], H), dtype=y.dtype, device=device), H
+    else:
+        lddy = _rows(dy, "dy", y.shape[0], H, y.dtype)
     if dweights is None:
         dweights = torch.empty((T, k), dtype=torch.float32, device=device)
-    if dweights.dtype != torch.float32 or dweights.shape != slot.shape or not dweights.is_contiguous():
+    elif dweights.dtype != torch.float32 or dweights.shape != slot.shape or not dweights.is_contiguous():
         raise TypeError("dweights must be a contiguous float32 tensor of slot's shape")
     call("expert_combine_grad", device, stream, T, k, H, code, dout.data_ptr(), ldo, y.data_ptr(), y.shape[0], ldy,
          slot.data_ptr(), w, dy.data_ptr(), lddy, dweights.data_ptr())
