@@ -155,29 +155,11 @@ Launch skinny_launch(const char* name) {
 
 // Skinny TN problems (at most 32 rows of A) stream B once with a split-K
 // kernel; everything else uses the block-tiled kernels.
-// Int8 has them with few rows on either side, up to 128.  Up to 32 the stream
-// of the many rows bounds the skinny kernel, and it always won.  Beyond, its
-// workgroups fetch (strip + few) rows of K bytes for every strip, at about 40
-// GB/s per CU, while the 128 x 128 block kernel takes 0.79 us per 128 k
-// whenever its tiles fit the CUs once (and in proportion when they do not):
-// equal where strips * (strip + few) / 256 CUs is 246 rows.  (us, bf16
-// results, skinny / block: 8192 x 64 x 8192 20.5 / 51.6, 8192 x 128 x 8192
-// 29.9 / 52.7, 20480 x 64 x 4096 30.6 / 32.2, 20480 x 128 x 4096 44.3 / 34.0,
-// 16384 x 128 x 8192 54.0 / 54.6, 57344 x 48 x 4096 69.0 / 54.7, 57344 x 32 x
-// 4096 50.5 / 53.6.)
-bool use_skinny(int dt, int layout, int64_t M, int64_t N) {
-  if (layout == DGEMM_TN && is_i8(dt)) {
-    const int64_t few = M < N ? M : N, many = M < N ? N : M;
-    if (few <= 32) return true;
-    if (few > kFewI8) return false;
-    const int64_t strip = i8_strip(many), work = (many + strip - 1) / strip * (strip + few);
-    return work <= 246 * kPlanCus * (many > 128 * kPlanCus ? (double)many / (128 * kPlanCus) : 1.0);
-  }
+bool use_skinny(int dt, int layout, int64_t M) {
   return layout == DGEMM_TN && (dt == DT_F16 || dt == DT_BF16) && M <= 32;
 }
 
-Launch select_skinny(int dt, int64_t M, int64_t N, int64_t K) {
-  if (is_i8(dt)) return skinny_i8_tn(dt - DT_I8, M <= N, M <= N ? M : N, M <= N ? N : M, K);
+Launch select_skinny(int dt, int64_t M) {
   if (dt == DT_F16) return M <= 16 ? skinny_launch<OpF16, 1>("f16_tn_skinny16") : skinny_launch<OpF16, 2>("f16_tn_skinny32");
   return M <= 16 ? skinny_launch<OpBF16, 1>("bf16_tn_skinny16") : skinny_launch<OpBF16, 2>("bf16_tn_skinny32");
 }
@@ -407,9 +389,10 @@ int plan(int dt, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, co
 
   Choice ch{};
   const bool forced = forced_choice(dt, layout == DGEMM_NN, K, &ch);
-  const bool skinny = !forced && use_skinny(dt, layout, M, N);
-  if (skinny) ch.L = select_skinny(dt, M, N, K);
-  else if (!forced) ch = choose(dt, layout, M, N, K);
+  const bool skinny = !forced && use_skinny(dt, layout, M);
+  const bool skinny8 = !forced && is_i8(dt) && layout == DGEMM_TN && skinny_i8_tn(dt - DT_I8, M, N, K, &ch.L);
+  if (skinny) ch.L = select_skinny(dt, M);
+  else if (!forced && !skinny8) ch = choose(dt, layout, M, N, K);
   const Launch L = ch.L;
   GemmArgs g{};
   if (!nn) {
@@ -481,7 +464,7 @@ int plan(int dt, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, co
     out->grid2 = g2.tiles_p * g2.tiles_q;
     if (out->grid2 > 0x7fffffff) return DGEMM_ERR_UNSUPPORTED;
   }
-  g.tiles_p = skinny && !is_i8(dt) ? 1 : (g.Pn + L.bp - 1) / L.bp;
+  g.tiles_p = skinny ? 1 : (g.Pn + L.bp - 1) / L.bp;
   g.tiles_q = (g.Qn + L.bq - 1) / L.bq;
   out->L = L;
   out->g = g;

@@ -170,22 +170,22 @@ __device__ __forceinline__ void gemm_i8_skinny_body(const GemmArgs& a, const Gat
   }
 }
 
-// One strip per workgroup of a dense product.
+// A dense product: one strip against at most FR of the few rows per workgroup.
 template <class Op, int SF, int FF, int NW, int D, bool FEWP>
 __global__ void __launch_bounds__(64 * NW) gemm_i8_skinny_kernel(const GemmArgs a) {
+  using Cfg = SkinnyI8Cfg<SF, FF, NW, D>;
+  const uint32_t tiles_p = (uint32_t)a.tiles_p;
+  const int64_t tq = (uint32_t)__builtin_amdgcn_readfirstlane((int)(blockIdx.x / tiles_p));
+  const int64_t p0 = (blockIdx.x - (uint32_t)tq * tiles_p) * (int64_t)(FEWP ? Cfg::FR : Cfg::SR);
+  const int64_t q0 = tq * (FEWP ? Cfg::SR : Cfg::FR);
   GemmArgs g = a;
-  const int64_t s0 = (int64_t)blockIdx.x * (16 * SF);
-  if constexpr (FEWP) {
-    g.Q += s0 * a.ldq;
-    g.C = (char*)a.C + s0 * a.ldc * Op::OE;
-    g.Qn = a.Qn - s0;
-    if (a.sq_row) g.sq += s0;
-  } else {
-    g.P += s0 * a.ldp;
-    g.C = (char*)a.C + s0 * Op::OE;
-    g.Pn = a.Pn - s0;
-    if (a.sp_row) g.sp += s0;
-  }
+  g.P += p0 * a.ldp;
+  g.Q += q0 * a.ldq;
+  g.C = (char*)a.C + (q0 * a.ldc + p0) * Op::OE;
+  g.Pn = a.Pn - p0;
+  g.Qn = a.Qn - q0;
+  if (a.sp_row) g.sp += p0;
+  if (a.sq_row) g.sq += q0;
   gemm_i8_skinny_body<Op, SF, FF, NW, D, FEWP, false>(g, Gather{});
 }
 

@@ -1,6 +1,8 @@
 // Int8 instantiations, FP32, FP16 and BF16 results: the eight-wave ping-pong
 // kernel (gemm_pp.hpp; TN, 256 x 256, with and without K-tail masks) and the
 // skinny kernel (gemm_i8_skinny.hpp; TN).
+#include <math.h>
+
 #include "dgemm.h"
 #include "gemm_i8_skinny.hpp"
 #include "gemm_pp.hpp"
@@ -25,7 +27,7 @@ Launch pp_launch(const char* name, bool kt) {
 template <class Op, int SF, int FF, int NW, int D>
 Launch skinny_launch(bool few_p) {
   using Cfg = SkinnyI8Cfg<SF, FF, NW, D>;
-  // (bp x bq: a strip of the one operand, all rows of the other)
+  // (bp x bq: a strip of the one operand, few rows of the other)
   if (few_p)
     return Launch{(const void*)&gemm_i8_skinny_kernel<Op, SF, FF, NW, D, true>, "i8_tn_skinny_a", Cfg::FR, Cfg::SR,
                   Cfg::NT, Cfg::LDS, false};
@@ -33,38 +35,60 @@ Launch skinny_launch(bool few_p) {
                 Cfg::NT, Cfg::LDS, false};
 }
 
-template <class Op, int FF>
-Launch skinny_few(bool few_p, int64_t many, int64_t K) {
-  if (i8_strip(many) == 32) {
-    // A second stage of copies in flight where a CU has one workgroup and the
-    // waves more than a stage each (bf16 results, 16 rows: 8192 x 8192 14.7
-    // us with two and 15.5 with one; 28672 x 8192 48.4 and 45.4; 5120 x 1040
-    // 5.1 and 4.3).
-    if constexpr (FF <= 2)
-      if (many <= 32 * 256 && K >= 2048) return skinny_launch<Op, 2, FF, 8, 2>(few_p);
-    return skinny_launch<Op, 2, FF, 8, 1>(few_p);
+template <class Op, int SF>
+Launch skinny(bool few_p, int ff, bool two) {
+  // Two stages of copies in flight where a CU has one workgroup and the waves
+  // more than a stage each, else one (bf16 results, 16 rows: 8192 x 8192 14.7
+  // us with two and 15.5 with one; 28672 x 8192 48.4 and 45.4; 5120 x 1040 5.1
+  // and 4.3; more than 32 few rows leave LDS for one).
+  switch (ff) {
+    case 1: return two ? skinny_launch<Op, SF, 1, 8, 2>(few_p) : skinny_launch<Op, SF, 1, 8, 1>(few_p);
+    case 2: return two ? skinny_launch<Op, SF, 2, 8, 2>(few_p) : skinny_launch<Op, SF, 2, 8, 1>(few_p);
+    case 4: return skinny_launch<Op, SF, 4, 8, 1>(few_p);
+    default: return skinny_launch<Op, SF, 8, 8, 1>(few_p);
   }
-  if constexpr (FF <= 2)
-    if (K >= 2048) return skinny_launch<Op, 1, FF, 8, 2>(few_p);
-  return skinny_launch<Op, 1, FF, 8, 1>(few_p);
-}
-
-template <class Op>
-Launch skinny(bool few_p, int64_t few, int64_t many, int64_t K) {
-  if (few <= 16) return skinny_few<Op, 1>(few_p, many, K);
-  if (few <= 32) return skinny_few<Op, 2>(few_p, many, K);
-  if (few <= 64) return skinny_few<Op, 4>(few_p, many, K);
-  return skinny_few<Op, 8>(few_p, many, K);
 }
 
 }  // namespace
 
-Launch skinny_i8_tn(int out, bool few_p, int64_t few, int64_t many, int64_t K) {
-  switch (out) {
-    case DGEMM_F32: return skinny<OpI8F>(few_p, few, many, K);
-    case DGEMM_F16: return skinny<OpI8H>(few_p, few, many, K);
-    default: return skinny<OpI8B>(few_p, few, many, K);
-  }
+// A workgroup of the skinny kernel fetches (strip + few) rows of K bytes at
+// about 40 GB/s per CU, whatever the rest does: its time is counted in rows per
+// CU, with fewer workgroups than CUs taking as long as one each.  The block
+// kernels in the same unit: 128 x 128 tiles 246 rows while there is at most
+// one per CU (0.79 us per 128 k) and 308 per two per CU, 256 x 256 tiles 410 a
+// round.  Up to 32 rows on one side the stream of the other bounds the
+// skinny kernel, and it always won.  (us, bf16 results, skinny / 128 x 128:
+// 8192 x 64 x 8192 20.5 / 51.6, 8192 x 128 x 8192 29.9 / 52.7, 20480 x 64 x
+// 4096 30.6 / 32.2, 20480 x 128 x 4096 44.3 / 34.0, 16384 x 128 x 8192 54.0 /
+// 54.6, 57344 x 48 x 4096 69.0 / 54.7, 57344 x 32 x 4096 50.5 / 53.6.)
+bool skinny_i8_tn(int out, int64_t Pn, int64_t Qn, int64_t K, Launch* L) {
+  constexpr double kCus = 256.0;
+  auto tiles = [](int64_t n, int64_t b) { return (double)((n + b - 1) / b); };
+  const bool few_p = Pn <= Qn;
+  const int64_t few = few_p ? Pn : Qn, many = few_p ? Qn : Pn;
+  int sf = 2, ff = 8;
+  double best = 0.0, wgs = 0.0;
+  for (int s = 1; s <= 2; ++s)
+    for (int f = 1; f <= 8; f *= 2) {
+      const double n = tiles(many, 16 * s) * tiles(few, 16 * f);
+      const double t = (n > kCus ? n / kCus : 1.0) * (16 * s + 16 * f);
+      if (best == 0.0 || t < best) {
+        best = t;
+        sf = s;
+        ff = f;
+        wgs = n;
+      }
+    }
+  const double t128 = tiles(Pn, 128) * tiles(Qn, 128), t256 = tiles(Pn, 256) * tiles(Qn, 256);
+  const double small = t128 <= kCus ? 246.0 : 308.0 * ceil(t128 / (2 * kCus)), large = 410.0 * ceil(t256 / kCus);
+  if (few > 32 && best > (small < large ? small : large)) return false;
+  const bool two = wgs <= kCus && K >= 2048;
+  auto pick = [&](auto op) {
+    using Op = decltype(op);
+    return sf == 1 ? skinny<Op, 1>(few_p, ff, two) : skinny<Op, 2>(few_p, ff, two);
+  };
+  *L = out == DGEMM_F32 ? pick(OpI8F{}) : (out == DGEMM_F16 ? pick(OpI8H{}) : pick(OpI8B{}));
+  return true;
 }
 
 Launch ping_pong_i8_tn(int out, bool kt) {

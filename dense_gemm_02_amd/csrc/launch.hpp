@@ -47,11 +47,9 @@ Launch four_wave_i8h_nn(int idx, bool kt);
 Launch four_wave_i8b_tn(int idx, bool kt);
 Launch four_wave_i8b_nn(int idx, bool kt);
 Launch ping_pong_i8_tn(int out, bool kt);   // out: dgemm_type
-// ... of at most kFewI8 rows of P (few_p) or Q with many of the other.
-// Strips of 32 of the many where that makes a strip per CU, else of 16.
-constexpr int64_t kFewI8 = 128;
-constexpr int i8_strip(int64_t many) { return many > 32 * 255 ? 32 : 16; }
-Launch skinny_i8_tn(int out, bool few_p, int64_t few, int64_t many, int64_t K);
+// Int8 with few rows on a side, or so few tiles that a long K leaves the CUs
+// idle: the skinny kernel's launch for Pn x Qn x K, or false.
+bool skinny_i8_tn(int out, int64_t Pn, int64_t Qn, int64_t K, Launch* L);
 
 // Keeps a HIP failure for dgemm_last_hip_error and returns DGEMM_ERR_HIP.
 int hip_failed(hipError_t e);

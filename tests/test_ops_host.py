@@ -40,7 +40,8 @@ def test_i8_scaled_refusals(lib):
     assert i8(lib, ldb=33) == ALIGN and i8(lib, C=FAKE + 2) == ALIGN and i8(lib, C=FAKE + 1, c=1) == ALIGN
     assert i8(lib, sa=FAKE + 2) == ALIGN and i8(lib, sb=FAKE + 1) == ALIGN
     assert i8(lib, K=131072, lda=131072, ldb=131072) == UNSUP
-    assert i8(lib, M=300, na=300, N=300, nb=300, lda=1 << 24, ldc=300) == UNSUP
+    assert i8(lib, M=300, na=300, N=300, nb=300, lda=1 << 27, ldc=300) == UNSUP
+    assert i8(lib, layout=0, M=300, na=300, lda=1 << 24) == UNSUP
 
 
 def test_i8_kernel_choice(lib):
@@ -56,7 +57,11 @@ def test_i8_kernel_choice(lib):
         assert name(t, 0, 8192, 8192, 8192) == f"{tag}_nn_256x256_w4"
         for layout in (0, 1):
             for K in (0, 1, 17, 4111):
-                assert name(t, layout, 300, 260, K).startswith(f"{tag}_{'tn' if layout else 'nn'}")
+                assert name(t, layout, 3000, 2600, K).startswith(f"{tag}_{'tn' if layout else 'nn'}")
+        # few rows on a side, or few tiles: strips of the other side
+        for M, N in ((1, 8192), (8192, 16), (28672, 32), (8192, 128), (300, 300), (512, 512)):
+            assert name(t, 1, M, N, 4096) == ("i8_tn_skinny_a" if M <= N else "i8_tn_skinny_b")
+        assert name(t, 1, 57344, 64, 4096).startswith(tag)
     assert lib.dgemm_kernel_config(9, 1, 4, 4, 4, buf, 256) == UNSUP
 
 
