@@ -8,6 +8,6 @@ not load the library; the first call does, and fails loudly if it is missing.
 
 from .binding import (gemm, gemm_f32, gemm_f16, gemm_bf16, gemm_fp8, gemm_fp8_scaled, gemm_mxfp8,  # noqa: F401
                       gemm_scaled, gemm_mx, matmul, gemm_strerror, DgemmError, library_path, load_library)
-from .quantized import quantize_i8, matmul_grouped  # noqa: F401
+from .quantized import quantize_i8, gemm_i8, matmul_grouped  # noqa: F401
 from .experts import (expert_sort, expert_dispatch, expert_dispatch_grad, expert_combine,  # noqa: F401
                       expert_combine_grad, matmul_experts)

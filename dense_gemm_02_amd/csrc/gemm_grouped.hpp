@@ -79,9 +79,11 @@ __device__ __forceinline__ bool group_tile(const GroupedArgs& A, GemmArgs* g, Ga
   int before = 0;
   if (groups > 64) {
     before = look(0, 0);
-    while (before <= m) before = look(e0 + 64, before);   // (m < mtiles, so it ends)
+    while (before <= m && e0 + 64 < groups) before = look(e0 + 64, before);
   }
-  const int src = __builtin_amdgcn_readfirstlane(__builtin_ctzll(__ballot(end > m)));
+  const uint64_t past = __ballot(end > m);
+  if (past == 0) return false;   // (offsets that do not ascend can add up to anything)
+  const int src = __builtin_amdgcn_readfirstlane(__builtin_ctzll(past));
   const int e = e0 + src;
   const int r0 = __builtin_amdgcn_readlane(lo, src), r1 = __builtin_amdgcn_readlane(hi, src);
   const uint32_t mt = (uint32_t)((r1 - r0 + BQ - 1) / BQ);

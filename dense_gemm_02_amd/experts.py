@@ -9,11 +9,12 @@ sorted by expert (-1: dropped).
 
 from __future__ import annotations
 
-from .quantized import call, matmul_grouped, one_device, pitch, quantize_i8, type_code
+from .quantized import call, matmul_grouped, one_device, pitch, quantize_i8, takes_stream, type_code
 from .binding import load_library
 
 
-def expert_sort(ids, experts, with_token=False, stream=None):
+@takes_stream
+def expert_sort(ids, experts, with_token=False):
     """Stable sort of the pairs by expert.
 
     ids: int64 or int32, [T, k], contiguous (a router's topk indices); an id
@@ -39,12 +40,8 @@ def expert_sort(ids, experts, with_token=False, stream=None):
     pair = buf.as_strided((n,), (1,), at + n)
     token = buf.as_strided((n,), (1,), at + 2 * n) if with_token else None
     need = load_library().expert_sort_workspace(T, k, experts)
-    ws = None
-    if need > 0:
-        ws = torch.empty((need,), dtype=torch.uint8, device=device)
-        if stream is not None:
-            ws.record_stream(stream if not isinstance(stream, int) else torch.cuda.ExternalStream(stream, device))
-    call("expert_sort", device, stream, T, k, experts, ids.data_ptr(), ids.element_size(), offsets.data_ptr(),
+    ws = torch.empty((need,), dtype=torch.uint8, device=device) if need > 0 else None
+    call("expert_sort", device, T, k, experts, ids.data_ptr(), ids.element_size(), offsets.data_ptr(),
          slot.data_ptr(), pair.data_ptr(), token.data_ptr() if with_token else None,
          ws.data_ptr() if ws is not None else None, max(need, 0))
     return (offsets, slot, pair, token) if with_token else (offsets, slot, pair)
@@ -72,7 +69,8 @@ def _rows(t, what, rows, H, dtype):
     return pitch(t, what)
 
 
-def expert_dispatch(x, slot, out=None, rows=None, stream=None):
+@takes_stream
+def expert_dispatch(x, slot, out=None, rows=None):
     """Rows to their sorted places: ``out[slot[t, j]] = x[t]``.  x: [T, H],
     float32, float16 or bfloat16.  A new out has ``rows`` (default T*k) rows;
     rows that no slot names are not written.  No slot may occur twice."""
@@ -86,12 +84,13 @@ def expert_dispatch(x, slot, out=None, rows=None, stream=None):
         out, ldy = torch.empty((T * k if rows is None else rows, H), dtype=x.dtype, device=device), H
     else:
         ldy = _rows(out, "out", rows, H, x.dtype)
-    call("expert_dispatch", device, stream, T, k, H, code, x.data_ptr(), ldx, slot.data_ptr(), out.data_ptr(),
+    call("expert_dispatch", device, T, k, H, code, x.data_ptr(), ldx, slot.data_ptr(), out.data_ptr(),
          out.shape[0], ldy)
     return out
 
 
-def expert_combine(y, slot, weights=None, out=None, stream=None):
+@takes_stream
+def expert_combine(y, slot, weights=None, out=None):
     """Sorted rows back to their tokens: ``out[t] = sum_j weights[t, j] *
     y[slot[t, j]]`` in float32, rounded once to y's dtype (weights None: all
     1).  A token with no pair left gets zeros."""
@@ -106,17 +105,19 @@ def expert_combine(y, slot, weights=None, out=None, stream=None):
         out, ldo = torch.empty((T, H), dtype=y.dtype, device=device), H
     else:
         ldo = _rows(out, "out", T, H, y.dtype)
-    call("expert_combine", device, stream, T, k, H, code, y.data_ptr(), y.shape[0], ldy, slot.data_ptr(), w,
+    call("expert_combine", device, T, k, H, code, y.data_ptr(), y.shape[0], ldy, slot.data_ptr(), w,
          out.data_ptr(), ldo)
     return out
 
 
-def expert_dispatch_grad(dy, slot, out=None, stream=None):
+@takes_stream
+def expert_dispatch_grad(dy, slot, out=None):
     """The gradient of ``expert_dispatch``: ``dx[t] = sum_j dy[slot[t, j]]``."""
-    return expert_combine(dy, slot, None, out=out, stream=stream)
+    return expert_combine(dy, slot, None, out=out)
 
 
-def expert_combine_grad(dout, y, slot, weights=None, dy=None, dweights=None, stream=None):
+@takes_stream
+def expert_combine_grad(dout, y, slot, weights=None, dy=None, dweights=None):
     """The gradients of ``expert_combine``: (dy, dweights) with
     ``dy[slot[t, j]] = weights[t, j] * dout[t]`` (rows that no slot names are
     not written) and ``dweights[t, j] = dout[t] . y[slot[t, j]]`` (float32, 0
@@ -138,12 +139,13 @@ def expert_combine_grad(dout, y, slot, weights=None, dy=None, dweights=None, str
         dweights = torch.empty((T, k), dtype=torch.float32, device=device)
     elif dweights.dtype != torch.float32 or dweights.shape != slot.shape or not dweights.is_contiguous():
         raise TypeError("dweights must be a contiguous float32 tensor of slot's shape")
-    call("expert_combine_grad", device, stream, T, k, H, code, dout.data_ptr(), ldo, y.data_ptr(), y.shape[0], ldy,
+    call("expert_combine_grad", device, T, k, H, code, dout.data_ptr(), ldo, y.data_ptr(), y.shape[0], ldy,
          slot.data_ptr(), w, dy.data_ptr(), lddy, dweights.data_ptr())
     return dy, dweights
 
 
-def matmul_experts(x, ids, weights, b, scale_b, out=None, stream=None):
+@takes_stream
+def matmul_experts(x, ids, weights, b, scale_b, out=None):
     """One linear layer of int8 experts: ``out[t] = sum_j weights[t, j] *
     (b[e] @ x[t])``, e = ids[t, j], with x quantised to int8 row by row.
 
@@ -152,15 +154,7 @@ def matmul_experts(x, ids, weights, b, scale_b, out=None, stream=None):
     ``matmul_grouped`` takes them.  Each token is quantised once; the products
     read its row through the sort, so no sorted copy of x is made.
     """
-    import contextlib
-    import torch
-    if stream is not None:
-        s = torch.cuda.ExternalStream(stream, x.device) if isinstance(stream, int) else stream
-        on = torch.cuda.stream(s)
-    else:
-        on = contextlib.nullcontext()
-    with on:
-        q, scale = quantize_i8(x)
-        offsets, slot, _, token = expert_sort(ids, b.shape[0], with_token=True)
-        y = matmul_grouped(q, b, offsets, scale, scale_b, out_dtype=x.dtype, row_index=token)
-        return expert_combine(y, slot, weights, out=out)
+    q, scale = quantize_i8(x)
+    offsets, slot, _, token = expert_sort(ids, b.shape[0], with_token=True)
+    y = matmul_grouped(q, b, offsets, scale, scale_b, out_dtype=x.dtype, row_index=token)
+    return expert_combine(y, slot, weights, out=out)

@@ -3,11 +3,14 @@ product with scales for each token and channel, and the products of a mixture
 of experts over sorted tokens.  Argument marshalling only, as ``binding``; the
 definitions are those of ``include/dgemm.h``.
 
-Every function takes ``stream`` (default: the current stream of the tensors'
-device) and runs on the tensors' device, whichever is current.
+Every function takes the keyword ``stream`` (a torch stream or a raw handle;
+default: the current stream of the tensors' device) and runs on the tensors'
+device, whichever is current.
 """
 
 from __future__ import annotations
+
+import functools
 
 from .binding import DgemmError, _device_tensors, _factor_vector, _need, load_library
 
@@ -26,27 +29,39 @@ def type_code(dtype):
     return code
 
 
-def call(name, device, stream, *args):
-    """One library call on `stream` with `device` current."""
+def call(name, device, *args):
+    """One library call on the current stream of `device`, with it current."""
     import torch
     # (The raw handle: building a Stream object costs as much as the rest of a
     # small call, 1.7 us.)
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
-    elif isinstance(stream, int):
-        handle = stream
-    else:
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-        handle = stream.cuda_stream
+    handle = torch._C._cuda_getCurrentRawStream(device.index)
     fn = getattr(load_library(), name)
-    if device.index == torch.cuda.current_device():
+    if device.index == torch._C._cuda_getDevice():
         st = fn(*args, handle)
     else:
         with torch.cuda.device(device):
             st = fn(*args, handle)
     if st != 0:
         raise DgemmError(st, name)
+
+
+def takes_stream(fn):
+    """Gives fn a keyword ``stream`` (a torch stream or a raw handle): the
+    call, and what it allocates, then belong to that stream, as under ``with
+    torch.cuda.stream(stream)``; inputs have to be ready on it."""
+    @functools.wraps(fn)
+    def with_stream(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        import torch
+        device = one_device("the arguments", args[0] if args else next(iter(kw.values()), None))
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return with_stream
 
 
 def one_device(names, first, *rest):
@@ -69,7 +84,8 @@ def pitch(t, what, align=1):
     return -(-max(cols, 1) // align) * align
 
 
-def quantize_i8(x, out=None, scale=None, stream=None):
+@takes_stream
+def quantize_i8(x, out=None, scale=None):
     """Rows of x (float32, float16 or bfloat16) to int8 with one scale each:
     ``scale[i] = max|x[i]| / 127``, ``q[i] = round(x[i] / scale[i])``.
 
@@ -98,7 +114,7 @@ def quantize_i8(x, out=None, scale=None, stream=None):
     elif scale.dtype != torch.float32 or scale.shape != (rows,) or not scale.is_contiguous():
         raise ValueError("scale must be a contiguous float32 tensor with one value a row")
     ldx = pitch(x, "x")
-    call("quantize_i8", device, stream, rows, K, x.data_ptr(), ldx, code, out.data_ptr(), ldq, scale.data_ptr())
+    call("quantize_i8", device, rows, K, x.data_ptr(), ldx, code, out.data_ptr(), ldq, scale.data_ptr())
     return out, scale
 
 
@@ -115,11 +131,13 @@ def gemm_i8(layout, M, N, K, A, lda, B, ldb, C, ldc, scale_a, scale_b, stream=No
     _factor_vector(scale_b, N, "scale_b")
     _check_extents(layout, M, N, K, A, lda, B, ldb, C, ldc, 1, C.element_size())
     lay = _LAYOUTS.get(layout, layout) if isinstance(layout, str) else layout
-    call("gemm_i8_scaled", device, stream, M, N, K, A.data_ptr(), lda, B.data_ptr(), ldb, C.data_ptr(), ldc, code,
-         scale_a.data_ptr(), scale_a.numel(), scale_b.data_ptr(), scale_b.numel(), lay)
+    run = takes_stream(lambda _, *args: call("gemm_i8_scaled", device, *args))
+    run(A, M, N, K, A.data_ptr(), lda, B.data_ptr(), ldb, C.data_ptr(), ldc, code,
+        scale_a.data_ptr(), scale_a.numel(), scale_b.data_ptr(), scale_b.numel(), lay, stream=stream)
 
 
-def matmul_i8(a, b, scale_a, scale_b, out=None, out_dtype=None, stream=None):
+@takes_stream
+def matmul_i8(a, b, scale_a, scale_b, out=None, out_dtype=None):
     """``binding.matmul`` for int8 operands: C = (A x B) * scale_a * scale_b,
     the layout read from b's strides as there."""
     import torch
@@ -152,12 +170,13 @@ def matmul_i8(a, b, scale_a, scale_b, out=None, out_dtype=None, stream=None):
     if M > 0 and N > 0 and K > 0:
         _need(a, M * lda, "a")
         _need(b, (K if layout == 0 else N) * ldb, "b")
-    call("gemm_i8_scaled", device, stream, M, N, K, a.data_ptr(), lda, b.data_ptr(), ldb, out.data_ptr(), ldc, code,
+    call("gemm_i8_scaled", device, M, N, K, a.data_ptr(), lda, b.data_ptr(), ldb, out.data_ptr(), ldc, code,
          scale_a.data_ptr(), scale_a.numel(), scale_b.data_ptr(), scale_b.numel(), layout)
     return out
 
 
-def matmul_grouped(a, b, offsets, scale_a, scale_b, out=None, out_dtype=None, row_index=None, stream=None):
+@takes_stream
+def matmul_grouped(a, b, offsets, scale_a, scale_b, out=None, out_dtype=None, row_index=None):
     """The int8 products of a mixture of experts over tokens sorted by expert:
     ``out[n] = (a[r] @ b[e].T) * (scale_a[r] * scale_b[e])`` for the rows n of
     expert e, ``offsets[e] <= n < offsets[e + 1]``, with r = n, or
@@ -204,7 +223,7 @@ def matmul_grouped(a, b, offsets, scale_a, scale_b, out=None, out_dtype=None, ro
     if rows > 0 and N > 0 and K > 0 and G > 0:
         _need(a, rows_a * lda, "a")
         _need(b, (G - 1) * group_b + N * ldb, "b")
-    call("gemm_i8_grouped", device, stream, G, rows, N, K, a.data_ptr(), rows_a, lda,
+    call("gemm_i8_grouped", device, G, rows, N, K, a.data_ptr(), rows_a, lda,
          row_index.data_ptr() if row_index is not None else None, b.data_ptr(), ldb, group_b, out.data_ptr(), ldc,
          code, scale_a.data_ptr(), scale_a.numel(), scale_b.data_ptr(), scale_b.numel(), offsets.data_ptr())
     return out

@@ -475,3 +475,53 @@ def test_results_repeat():
     for _ in range(3):
         for a, b in zip(first, (L.expert_combine(y, slot, w), *L.expert_combine_grad(d, y, slot, w, dy=dy))):
             assert torch.equal(a, b)
+
+
+def test_python_refusals():
+    L = lib()
+    ids = torch.zeros((6, 2), dtype=torch.int64, device="cuda")
+    slot = torch.arange(12, dtype=torch.int32, device="cuda").reshape(6, 2)
+    x, y = torch.randn((6, 8), device="cuda"), torch.randn((12, 8), device="cuda")
+    w = torch.rand((6, 2), device="cuda")
+    value = [
+        lambda: L.expert_sort(ids.reshape(-1), 3), lambda: L.expert_sort(ids[:, :1], 3), lambda: L.expert_sort(ids, -1),
+        lambda: L.expert_dispatch(y, slot), lambda: L.expert_dispatch(x, slot, out=y.half()),
+        lambda: L.expert_dispatch(x, slot, out=y[:, :7]), lambda: L.expert_dispatch(x, slot, rows=11, out=y),
+        lambda: L.expert_dispatch(x.t().contiguous().t(), slot), lambda: L.expert_combine(y, slot, w, out=y),
+        lambda: L.expert_combine_grad(y, y, slot, w), lambda: L.expert_combine_grad(x, y, slot, w, dy=x),
+        lambda: L.expert_combine_grad(x.half(), y, slot, w),
+    ]
+    kind = [
+        lambda: L.expert_sort(ids.float(), 3), lambda: L.expert_dispatch(x, slot.long()),
+        lambda: L.expert_combine(y.double(), slot), lambda: L.expert_combine(y, slot, w.half()),
+        lambda: L.expert_combine(y, slot, w[:5]), lambda: L.expert_combine(y, slot[:, :1]),
+        lambda: L.expert_combine_grad(x, y, slot, w, dweights=w.half()),
+    ]
+    for calls, error in ((value, ValueError), (kind, TypeError)):
+        for i, c in enumerate(calls):
+            with pytest.raises(error):
+                c()
+                print("not refused:", error, i)
+    with pytest.raises(L.DgemmError) as e:
+        L.expert_sort(ids, 1025)
+    assert e.value.status == 6
+    with pytest.raises(L.DgemmError) as e:        # rows of pitch 0
+        L.expert_dispatch(x[:1].expand(6, 8), slot)
+    assert e.value.status == 3
+
+
+def test_streams_by_argument():
+    """Work given a stream is that stream's, its results and workspace too."""
+    L = lib()
+    ids, w, _, slot, pair = routing(5000, 4, 40, 9)
+    x = rows(gen(2), 5000, 256, torch.bfloat16)
+    b = torch.randint(-127, 128, (40, 64, 256), generator=gen(3), device="cuda", dtype=torch.int8)
+    sb = torch.rand((40, 64), generator=gen(4), device="cuda")
+    want = L.matmul_experts(x, ids, w, b, sb)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        _, slot2, pair2 = L.expert_sort(ids, 40, stream=stream)
+        got = L.matmul_experts(x, ids, w, b, sb, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(slot2, slot) and torch.equal(pair2, pair) and torch.equal(got, want)

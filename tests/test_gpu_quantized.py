@@ -466,3 +466,89 @@ def test_on_a_side_stream_and_captured():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, layer())
+
+
+def test_stream_arguments():
+    """A stream by object, by raw handle and the null stream's handle."""
+    L = lib()
+    x = torch.randn((20, 300), generator=gen(1), device="cuda")
+    q, s = L.quantize_i8(x)
+    w, sw = ints(gen(2), (50, 300)), factors(gen(3), 50)
+    want = L.matmul(w, q.t(), scale_a=sw, scale_b=s)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream, 0):
+        q2, s2 = L.quantize_i8(x=x, stream=stream)
+        y = L.matmul(w, q2.t(), scale_a=sw, scale_b=s2, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(q2, q) and torch.equal(s2, s) and torch.equal(y, want)
+
+
+@pytest.mark.parametrize("layout", ["tn", "nn"])
+def test_gemm_i8_on_storage(layout):
+    """The tensor-level call with pitches of its own, and what it refuses."""
+    L = lib()
+    M, N, K, ld = 40, 50, 70, 96
+    g = gen(4)
+    A = torch.randint(-128, 128, (M, ld), generator=g, device="cuda", dtype=torch.int8)
+    B = torch.randint(-128, 128, (N if layout == "tn" else K, ld), generator=g, device="cuda", dtype=torch.int8)
+    sa, sb = factors(g, M), factors(g, N)
+    b = B[:, :K].t() if layout == "tn" else B[:, :N]
+    for dtype in TYPES:
+        C = torch.zeros((N if layout == "tn" else M, 64), device="cuda").to(dtype)
+        L.gemm_i8(layout, M, N, K, A, ld, B, ld, C, 64, sa, sb)
+        got = C[:, :M].t() if layout == "tn" else C[:, :N]
+        near(got, exact(A[:, :K], b, sa, sb))
+    with pytest.raises(ValueError):
+        L.gemm_i8(layout, M + 1, N, K, A, ld, B, ld, C, 64, torch.ones(1, device="cuda"), sb)
+    with pytest.raises(ValueError):
+        L.gemm_i8(layout, M, N, K, A, ld, B, ld, C[:-1].clone(), 64, sa, sb)
+    with pytest.raises(ValueError):
+        L.gemm_i8(layout, M, N, K, A, ld, B, ld, C, 64, sa[:5], sb)
+    with pytest.raises(TypeError):
+        L.gemm_i8(layout, M, N, K, A, ld, B, ld, C.to(torch.int32), 64, sa, sb)
+    with pytest.raises(L.DgemmError):
+        L.gemm_i8(layout, M, N, K, A, ld - 8, B, ld, C, 64, sa, sb)
+
+
+def test_python_refusals():
+    L = lib()
+    g = gen(6)
+    q, s = ints(g, (40, 64)), factors(g, 40)
+    w, sw = ints(g, (50, 64)), factors(g, 50)
+    one = torch.ones(1, device="cuda")
+    x = torch.randn((4, 8), device="cuda")
+    off = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+    wide = torch.empty((50, 40), device="cuda").t()
+    value = [
+        lambda: L.matmul(q, w.t()), lambda: L.matmul(q, w.t(), scale_a=s),
+        lambda: L.matmul(q, w, scale_a=s, scale_b=sw), lambda: L.matmul(q, w.t(), scale_a=s[:7], scale_b=sw),
+        lambda: L.matmul(q, w.t(), scale_a=s, scale_b=sw, out=wide[:, :49]),
+        lambda: L.matmul(q, w.t(), scale_a=s, scale_b=sw, out=wide, out_dtype=torch.float16),
+        lambda: L.matmul(q[:, ::2], w[:, ::2].t(), scale_a=s, scale_b=sw),
+        lambda: L.quantize_i8(x[0]), lambda: L.quantize_i8(x.t()), lambda: L.quantize_i8(x, out=q),
+        lambda: L.quantize_i8(x, scale=s), lambda: L.matmul_grouped(q, w, off, s, sw),
+        lambda: L.matmul_grouped(q, w[None, :, :32], off, s, sw), lambda: L.matmul_grouped(q, w[None], off, s[:3], sw),
+        lambda: L.matmul_grouped(q, w[None], off, s, sw[:3]),
+        lambda: L.matmul_grouped(q, w[None], off, s, sw, out=torch.empty((39, 50), device="cuda")),
+    ]
+    kind = [
+        lambda: L.matmul(q, x.t(), scale_a=s, scale_b=sw), lambda: L.matmul(q, w.t(), scale_a=s.double(), scale_b=sw),
+        lambda: L.matmul(q, w.t(), scale_a=s, scale_b=sw, out_dtype=torch.int32),
+        lambda: L.quantize_i8(x.double()), lambda: L.quantize_i8(q),
+        lambda: L.matmul_grouped(x, w[None], off, s, sw), lambda: L.matmul_grouped(q, w[None], off.long(), s, sw),
+        lambda: L.matmul_grouped(q, w[None], off[:1], s, sw),
+        lambda: L.matmul_grouped(q, w[None], off, s, sw, row_index=off.long()),
+        lambda: L.matmul(x, x.t(), out_dtype=torch.float16),
+    ]
+    for calls, error in ((value, ValueError), (kind, TypeError)):
+        for i, c in enumerate(calls):
+            with pytest.raises(error):
+                c()
+                print("not refused:", error, i)
+    odd = torch.zeros((4, 20), dtype=torch.int8, device="cuda")      # a pitch of 20 bytes
+    with pytest.raises(L.DgemmError) as e:
+        L.matmul(odd, odd.t(), scale_a=one, scale_b=one)
+    assert e.value.status == 5
+    with pytest.raises(ValueError):                                  # a row's last 16 bytes have to be there
+        L.matmul(odd[:1, :5].clone(), odd[:1, :5].clone().t(), scale_a=one, scale_b=one)
