@@ -50,7 +50,7 @@ def units():
     """(source, object, extra flags) of every translation unit."""
     out = [(os.path.join(CSRC, "dgemm.hip"), os.path.join(OBJDIR, "dgemm.o"), []),
            (os.path.join(CSRC, "pp.hip"), os.path.join(OBJDIR, "pp.o"), [])]
-    for name in ("i8", "grouped", "quantize", "experts"):
+    for name in ("i8", "i8_nn", "grouped", "quantize", "experts"):
         out.append((os.path.join(CSRC, name + ".hip"), os.path.join(OBJDIR, name + ".o"), []))
     for tag, op, nn in FOUR_WAVE:
         out.append((os.path.join(CSRC, "four_wave.hip"), os.path.join(OBJDIR, f"four_wave_{tag}.o"),

@@ -390,7 +390,9 @@ int plan(int dt, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, co
   Choice ch{};
   const bool forced = forced_choice(dt, layout == DGEMM_NN, K, &ch);
   const bool skinny = !forced && use_skinny(dt, layout, M);
-  const bool skinny8 = !forced && is_i8(dt) && layout == DGEMM_TN && skinny_i8_tn(dt - DT_I8, M, N, K, &ch.L);
+  const bool skinny8 = !forced && is_i8(dt) &&
+                       (layout == DGEMM_TN ? skinny_i8_tn(dt - DT_I8, M, N, K, &ch.L)
+                                           : skinny_i8_nn(dt - DT_I8, N, M, &ch.L));
   if (skinny) ch.L = select_skinny(dt, M);
   else if (!forced && !skinny8) ch = choose(dt, layout, M, N, K);
   const Launch L = ch.L;

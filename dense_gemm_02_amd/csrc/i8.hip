@@ -44,8 +44,8 @@ Launch skinny(bool few_p, int ff, bool two) {
   switch (ff) {
     case 1: return two ? skinny_launch<Op, SF, 1, 8, 2>(few_p) : skinny_launch<Op, SF, 1, 8, 1>(few_p);
     case 2: return two ? skinny_launch<Op, SF, 2, 8, 2>(few_p) : skinny_launch<Op, SF, 2, 8, 1>(few_p);
-    case 4: return skinny_launch<Op, SF, 4, 8, 1>(few_p);
-    default: return skinny_launch<Op, SF, 8, 8, 1>(few_p);
+    case 4: return skinny_launch<Op, 2, 4, 8, 1>(few_p);
+    default: return skinny_launch<Op, 2, 8, 8, 1>(few_p);
   }
 }
 
@@ -70,6 +70,7 @@ bool skinny_i8_tn(int out, int64_t Pn, int64_t Qn, int64_t K, Launch* L) {
   double best = 0.0, wgs = 0.0;
   for (int s = 1; s <= 2; ++s)
     for (int f = 1; f <= 8; f *= 2) {
+      if (s == 1 && f > 2) continue;   // (as many workgroups as half the few rows and strips of 32, more to fetch)
       const double n = tiles(many, 16 * s) * tiles(few, 16 * f);
       const double t = (n > kCus ? n / kCus : 1.0) * (16 * s + 16 * f);
       if (best == 0.0 || t < best) {

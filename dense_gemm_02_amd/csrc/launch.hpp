@@ -50,6 +50,7 @@ Launch ping_pong_i8_tn(int out, bool kt);   // out: dgemm_type
 // Int8 with few rows on a side, or so few tiles that a long K leaves the CUs
 // idle: the skinny kernel's launch for Pn x Qn x K, or false.
 bool skinny_i8_tn(int out, int64_t Pn, int64_t Qn, int64_t K, Launch* L);
+bool skinny_i8_nn(int out, int64_t Pn, int64_t Qn, Launch* L);
 
 // Keeps a HIP failure for dgemm_last_hip_error and returns DGEMM_ERR_HIP.
 int hip_failed(hipError_t e);

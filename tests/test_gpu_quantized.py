@@ -210,6 +210,38 @@ def test_product_few_rows(many, dtype):
             a, b, sa, sb = operands("tn", few, many, K, few + many + K, pad=K % 2)
             near(lib().matmul(a, b, scale_a=sa, scale_b=sb, out_dtype=dtype), exact(a, b, sa, sb))
             near(lib().matmul(b.t(), a.t(), scale_a=sb, scale_b=sa, out_dtype=dtype), exact(b.t(), a.t(), sb, sa))
+            a, b, sa, sb = operands("nn", few, many, K, few + many + K, pad=K % 2)
+            near(lib().matmul(a, b, scale_a=sa, scale_b=sb, out_dtype=dtype), exact(a, b, sa, sb))
+            a, b, sa, sb = operands("nn", many, few, K, few + many + K, pad=K % 2)
+            near(lib().matmul(a, b, scale_a=sa, scale_b=sb, out_dtype=dtype), exact(a, b, sa, sb))
+
+
+# (M, N) that make the skinny kernels take each of their tiles (p x q).
+SKINNY = [
+    ("nn", "16x16", 3, 5), ("nn", "16x16", 37, 212), ("nn", "16x32", 4428, 11), ("nn", "32x16", 7, 5018),
+    ("nn", "32x32", 17, 5077), ("nn", "32x64", 4728, 33), ("nn", "32x128", 65, 5544), ("nn", "64x16", 2, 11341),
+    ("nn", "64x32", 19, 11294), ("nn", "64x64", 33, 11088), ("nn", "64x128", 67, 11757), ("nn", "128x16", 1, 26184),
+    ("nn", "128x32", 17, 26188), ("nn", "128x64", 34, 29448),
+    ("tn", "128x32", 69, 7056), ("tn", "16x16", 5, 9), ("tn", "16x32", 3, 6219), ("tn", "32x16", 20, 3269),
+    ("tn", "32x32", 18, 5677), ("tn", "64x32", 34, 6335), ("tn", "16x32", 3170, 18), ("tn", "32x128", 6845, 65),
+    ("tn", "32x16", 6174, 1), ("tn", "32x32", 5601, 18), ("tn", "32x64", 6295, 35), ("tn", "16x32", 300, 511)]
+
+
+@pytest.mark.parametrize("layout,tile,M,N", SKINNY)
+def test_product_every_skinny_tile(layout, tile, M, N):
+    """K below a stage (128), a whole number of stages, ending inside one and
+    inside a chunk, and more stages than waves; factors one or one a row."""
+    import ctypes
+    L = lib()
+    buf = ctypes.create_string_buffer(256)
+    for K in (1, 100, 128, 500, 1024, 2100, 2560):
+        assert L.load_library().dgemm_kernel_config(7, 1 if layout == "tn" else 0, M, N, K, buf, 256) == 0
+        assert "skinny" in buf.value.decode() and f"tile={tile} " in buf.value.decode(), buf.value
+        a, b, sa, sb = operands(layout, M, N, K, M + N + K, pad=K % 3)
+        for dtype in TYPES:
+            print(f"skinny {layout} {tile} {M}x{N}x{K} {dtype}", flush=True)
+            near(L.matmul(a, b, scale_a=sa, scale_b=sb, out_dtype=dtype), exact(a, b, sa, sb))
+        near(L.matmul(a, b, scale_a=sa[:1], scale_b=sb[:1]), exact(a, b, sa[:1], sb[:1]))
 
 
 TILES_TN = ["256x256_w4", "128x128_w4", "128x128_w4_s4", "192x256_w4", "256x192_w4", "256x256_pp"]

@@ -41,7 +41,7 @@ def test_i8_scaled_refusals(lib):
     assert i8(lib, sa=FAKE + 2) == ALIGN and i8(lib, sb=FAKE + 1) == ALIGN
     assert i8(lib, K=131072, lda=131072, ldb=131072) == UNSUP
     assert i8(lib, M=300, na=300, N=300, nb=300, lda=1 << 27, ldc=300) == UNSUP
-    assert i8(lib, layout=0, M=300, na=300, lda=1 << 24) == UNSUP
+    assert i8(lib, layout=0, M=300, na=300, lda=1 << 27) == UNSUP
 
 
 def test_i8_kernel_choice(lib):
@@ -55,6 +55,7 @@ def test_i8_kernel_choice(lib):
     for t, tag in ((0, "i8f"), (1, "i8h"), (2, "i8b")):
         assert name(t, 1, 8192, 8192, 8192) == f"{tag}_tn_256x256_pp"
         assert name(t, 0, 8192, 8192, 8192) == f"{tag}_nn_256x256_w4"
+        assert name(t, 0, 16, 8192, 8192) == name(t, 0, 300, 300, 1000) == "i8_nn_skinny"
         for layout in (0, 1):
             for K in (0, 1, 17, 4111):
                 assert name(t, layout, 3000, 2600, K).startswith(f"{tag}_{'tn' if layout else 'nn'}")
