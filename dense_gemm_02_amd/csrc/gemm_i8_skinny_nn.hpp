@@ -15,6 +15,8 @@
 // zeros, so nothing of Q needs masking: what lies behind K in its rows
 // meets zeros.  Workgroups next to each other along p run on one XCD at the
 // same time: a 128-byte line of B that two narrow strips share is fetched once.
+// The latency of rows a pitch apart bounds it: 16 x 8192 x 8192 28 us, 2.4 TB/s
+// (with B in the caches 20), against 12.4 for a B contiguous along K.
 #pragma once
 
 #include "common.hpp"

@@ -242,8 +242,8 @@ int quantize_i8(int64_t rows, int64_t K, const void* X, int64_t ldx, int x_type,
  * In all three a slot outside 0 .. rows - 1 (rows: of Y and dY) counts as
  * dropped; a slot must not occur twice where rows are written.  `type` is the
  * dgemm_type of every row matrix; pitches are in elements, at least H; no
- * alignment beyond that of the elements.  Results do not depend on timing:
- * no atomics are used.
+ * alignment beyond that of the elements.  Every result is the same from run
+ * to run.
  * Checks: type (id_bytes); negative sizes -> DGEMM_ERR_INVALID_DIM; nothing
  * to do -> DGEMM_OK; NULL pointers; leading dimensions; alignment; limits
  * (tokens*k, rows or H above 2^31 - 1 -> DGEMM_ERR_UNSUPPORTED).
