@@ -438,8 +438,8 @@ int plan(int dt, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, co
   if (K * e > kMaxDescBytes || (is_i8(dt) && K > kMaxI8K)) return DGEMM_ERR_UNSUPPORTED;
   g.group = 8;
   const int oe = out_elem(dt);
-  g.vec_store = ((((uintptr_t)C) % (uintptr_t)(4 * oe)) == 0 && ((ldc * oe) % (4 * oe)) == 0) ? 1 : 0;
-  g.vec16 = ((((uintptr_t)C) % 16) == 0 && ((ldc * oe) % 16) == 0) ? 1 : 0;
+  g.vec_store = ((((uintptr_t)C) % (uintptr_t)(4 * oe)) == 0 && ldc % 4 == 0) ? 1 : 0;
+  g.vec16 = ((((uintptr_t)C) % 16) == 0 && ldc % (16 / oe) == 0) ? 1 : 0;
   if (ch.split) {
     // The second launch covers q >= at (rows of Q and of the factor / scale
     // arrays along q, columns of D) or p >= at (rows of P -- for

@@ -180,7 +180,7 @@ extern "C" int gemm_i8_grouped(int64_t groups, int64_t rows, int64_t N, int64_t 
   g.C = C; g.ldc = ldc; g.K = K;
   g.group = 8;
   g.vec_store = aligned(C, 4 * oe) && ldc % 4 == 0;
-  g.vec16 = aligned(C, 16) && (ldc * oe) % 16 == 0;
+  g.vec16 = aligned(C, 16) && ldc % (16 / oe) == 0;
   g.sp = scale_b; g.sp_row = n_scale_b > 1 ? 1 : 0;
   g.sq = scale_a; g.sq_row = n_scale_a > 1 ? 1 : 0;
   a.offsets = offsets; a.groups = groups; a.rows = rows; a.pstride = group_b;

@@ -440,6 +440,53 @@ def test_layer_captured_into_a_graph_with_eager_work_between():
             assert torch.equal(got, want)
 
 
+def test_two_graphs_in_turn():
+    """Two captured graphs with a sort that needs its workspace, replayed in
+    turn with eager calls between."""
+    L = lib()
+    state, graphs = [], []
+    for seed, (T, k, E) in ((1, (3000, 4, 40)), (2, (5000, 2, 700))):
+        ids = routing(T, k, E, seed)[0]
+        x = rows(gen(seed), T, 200, torch.bfloat16)
+        w = torch.rand((T, k), generator=gen(seed), device="cuda")
+
+        def step(ids=ids, x=x, w=w, E=E):
+            offsets, slot, pair = L.expert_sort(ids, E)
+            return offsets, slot, pair, L.expert_combine(L.expert_dispatch(x, slot), slot, w)
+
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        state.append((ids, step, out, (T, k, E)))
+        graphs.append(graph)
+    for turn in range(3):
+        for (ids, _, _, shape), graph in zip(state, graphs):
+            ids.copy_(routing(*shape, 50 + turn)[0])
+        for graph in graphs:
+            graph.replay()
+        for _, step, out, _ in state:
+            for got, want in zip(out, step()):
+                assert torch.equal(got, want)
+
+
+def test_layer_without_pairs():
+    """No token, and tokens that no expert takes."""
+    L = lib()
+    b = torch.ones((3, 32, 64), dtype=torch.int8, device="cuda")
+    sb = torch.ones((3, 32), device="cuda")
+    none = L.matmul_experts(torch.ones((0, 64), device="cuda"), torch.zeros((0, 2), dtype=torch.int64, device="cuda"),
+                            torch.ones((0, 2), device="cuda"), b, sb)
+    assert none.shape == (0, 32)
+    x = torch.randn((5, 64), generator=gen(1), device="cuda").half()
+    out = L.matmul_experts(x, torch.full((5, 2), -1, device="cuda"), torch.ones((5, 2), device="cuda"), b, sb)
+    assert out.shape == (5, 32) and out.dtype == torch.float16 and (out == 0).all()
+    one = L.matmul_experts(x[:1], torch.full((1, 1), 2, device="cuda"), None, b, sb)
+    q, s = L.quantize_i8(x[:1])
+    near(one, q.double().sum(1, keepdim=True).expand(1, 32) * s.double()[:, None], 6 * 2.0 ** -24 * 64 * 127 * s.double()[:, None])
+
+
 def test_two_streams_at_once():
     L = lib()
     cases = []
