@@ -89,6 +89,12 @@ bool k_tail(int dt, int64_t K) { return K % (128 / in_elem(dt)) != 0; }
 // number of rounds of workgroups times the time of one round ("FP16 GEMM
 // Optimization on AMD RDNA 3 and RDNA 4", Where That Leaves Us: no single
 // tile is best on every shape).
+// 64 x 128 (int8 TN) fills CUs that 128 x 128 leaves idle when one side is a
+// few hundred tokens; with four stages, one per CU, for one round (us, bf16
+// results, 64 x 128 with four / two stages, then the better 128 x 128: 8192 x
+// 256 x 8192 33.5 / 54.3 / 52.2, 4096 x 512 x 4096 19.2 / 22.5 / 26.9, 1536 x
+// 700 x 2048 12.6 / 13.6 / 17.1; 2048^3, two rounds 22.9 / 15.8 / 18.1; 4096 x
+// 1024 x 4096 34.3 / 25.2 / 28.1).
 struct TileChoice {
   int bp, bq, per_cu;   // tile, workgroups resident per CU
   double rate;          // CU throughput relative to 256 x 256
@@ -99,7 +105,9 @@ constexpr TileChoice kTiles[kNumTiles] = {{256, 256, 1, 1.00, 0},
                                           {128, 128, 2, 0.78, 0},
                                           {128, 128, 1, 0.47, 1},
                                           {192, 256, 1, 0.87, 1},
-                                          {256, 192, 1, 0.87, 1}};
+                                          {256, 192, 1, 0.87, 1},
+                                          {64, 128, 2, 0.457, 0},
+                                          {64, 128, 1, 0.333, 1}};
 constexpr int kPlanCus = 256;  // MI355X CUs, for the tile choice only
 
 int pick_tile(int64_t Pn, int64_t Qn, unsigned allowed, double* cost = nullptr) {
@@ -133,7 +141,7 @@ unsigned tile_mask(int dt, bool nn, int64_t K) {
   // results, four / two stages: 2048 x 2048 x 1024 15.7 / 12.9, x 4096 31.0 /
   // 27.8, x 8192 52.3 / 58.8; with tail masks 1536 x 1536 x 6000 37.1 / 47.6,
   // 2000 x 1500 x 3001 21.1 / 25.8).
-  if (is_i8(dt) && K <= 4096 && K % 128 == 0) return 0b0101u | t192;
+  if (is_i8(dt) && !nn) return (K <= 4096 && K % 128 == 0 ? 0b11000101u : 0b11001101u) | t192;
   return (dt == DT_MX8 ? 0b0101u : 0b1101u) | t192;
 }
 

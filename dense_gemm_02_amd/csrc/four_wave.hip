@@ -48,6 +48,13 @@ Launch DG_FN(int idx, bool kt) {
         // The MX scale ring needs two LDS stages.
         if constexpr (!Op::MX) return tn_launch<Op, PKM, 128, 128, 4>(DG_NAME("128x128_w4_s4"), kt);
         [[fallthrough]];
+      case 6:
+      case 7:
+        // Built for int8 TN only.
+        if constexpr (!PKM && Op::TRIM)
+          return idx == 6 ? tn_launch<Op, PKM, 64, 128>(DG_NAME("64x128_w4"), kt)
+                          : tn_launch<Op, PKM, 64, 128, 4>(DG_NAME("64x128_w4_s4"), kt);
+        [[fallthrough]];
       default: return tn_launch<Op, PKM, 256, 256>(DG_NAME("256x256_w4"), kt);
     }
   }

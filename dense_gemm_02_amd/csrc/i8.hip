@@ -55,13 +55,14 @@ Launch skinny(bool few_p, int ff, bool two) {
 // A workgroup of the skinny kernel fetches (strip + few) rows of K bytes at
 // about 40 GB/s per CU, whatever the rest does: its time is counted in rows per
 // CU, with fewer workgroups than CUs taking as long as one each.  The block
-// kernels in the same unit: 128 x 128 tiles 246 rows while there is at most
-// one per CU (0.79 us per 128 k) and 308 per two per CU, 256 x 256 tiles 410 a
-// round.  Up to 32 rows on one side the stream of the other bounds the
-// skinny kernel, and it always won.  (us, bf16 results, skinny / 128 x 128:
-// 8192 x 64 x 8192 20.5 / 51.6, 8192 x 128 x 8192 29.9 / 52.7, 20480 x 64 x
-// 4096 30.6 / 32.2, 20480 x 128 x 4096 44.3 / 34.0, 16384 x 128 x 8192 54.0 /
-// 54.6, 57344 x 48 x 4096 69.0 / 54.7, 57344 x 32 x 4096 50.5 / 53.6.)
+// kernels in the same unit: 64 x 128 tiles 185 rows while there is at most one
+// per CU and 230 with two, 128 x 128 tiles 308 per two per CU, 256 x 256 tiles
+// 410 a round.  Up to 32 rows on one side the stream of the other bounds the
+// skinny kernel, and it always won.  (us, bf16 results, skinny / the best
+// block kernel: 8192 x 64 x 8192 20.5 / 32, 8192 x 128 x 8192 29.2 / 33, 8192 x
+// 160 x 8192 57 / 32, 4096 x 256 x 4096 13.6 / 18.1, 1024 x 1024 x 4096 15.2 /
+// 18.2, 1536 x 700 x 2048 15.6 / 12.6, 28672 x 64 x 8192 68 / 57, 57344 x 32 x
+// 4096 50.5 / 53.6.)
 bool skinny_i8_tn(int out, int64_t Pn, int64_t Qn, int64_t K, Launch* L) {
   constexpr double kCus = 256.0;
   auto tiles = [](int64_t n, int64_t b) { return (double)((n + b - 1) / b); };
@@ -73,7 +74,9 @@ bool skinny_i8_tn(int out, int64_t Pn, int64_t Qn, int64_t K, Launch* L) {
     for (int f = 1; f <= 8; f *= 2) {
       if (s == 1 && f > 2) continue;   // (as many workgroups as half the few rows and strips of 32, more to fetch)
       const double n = tiles(many, 16 * s) * tiles(few, 16 * f);
-      const double t = (n > kCus ? n / kCus : 1.0) * (16 * s + 16 * f);
+      // (From 64 few rows on a CU's LDS holds one workgroup, so rounds are whole.)
+      const double rounds = f >= 4 ? ceil(n / kCus) : (n > kCus ? n / kCus : 1.0);
+      const double t = rounds * (16 * s + 16 * f);
       if (best == 0.0 || t < best) {
         best = t;
         sf = s;
@@ -81,8 +84,10 @@ bool skinny_i8_tn(int out, int64_t Pn, int64_t Qn, int64_t K, Launch* L) {
         wgs = n;
       }
     }
-  const double t128 = tiles(Pn, 128) * tiles(Qn, 128), t256 = tiles(Pn, 256) * tiles(Qn, 256);
-  const double small = t128 <= kCus ? 246.0 : 308.0 * ceil(t128 / (2 * kCus)), large = 410.0 * ceil(t256 / kCus);
+  const double t64 = tiles(Pn, 64) * tiles(Qn, 128), t128 = tiles(Pn, 128) * tiles(Qn, 128);
+  const double t256 = tiles(Pn, 256) * tiles(Qn, 256);
+  const double small = t64 <= kCus ? 185.0 : (t64 <= 2 * kCus ? 230.0 : 308.0 * ceil(t128 / (2 * kCus)));
+  const double large = 410.0 * ceil(t256 / kCus);
   if (few > 32 && best > (small < large ? small : large)) return false;
   const bool two = wgs <= kCus && K >= 2048;
   auto pick = [&](auto op) {

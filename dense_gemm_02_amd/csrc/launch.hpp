@@ -18,8 +18,9 @@ struct Launch {
 
 // Entries of the block-tile table of the four-wave kernel (dgemm.hip,
 // kTiles): 0 256x256, 1 256x128, 2 128x128 (two workgroups per CU),
-// 3 128x128 with four LDS stages, 4 192x256, 5 256x192.
-constexpr int kNumTiles = 6;
+// 3 128x128 with four LDS stages, 4 192x256, 5 256x192, and for int8 TN
+// 6 64x128 (two workgroups per CU), 7 64x128 with four LDS stages.
+constexpr int kNumTiles = 8;
 
 // The four-wave launch of table entry `idx` for one input format and layout
 // (`kt`: K ends inside a stage, so the copies need tail masks).  Entries a

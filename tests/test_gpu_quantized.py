@@ -244,7 +244,8 @@ def test_product_every_skinny_tile(layout, tile, M, N):
         near(L.matmul(a, b, scale_a=sa[:1], scale_b=sb[:1]), exact(a, b, sa[:1], sb[:1]))
 
 
-TILES_TN = ["256x256_w4", "128x128_w4", "128x128_w4_s4", "192x256_w4", "256x192_w4", "256x256_pp"]
+TILES_TN = ["256x256_w4", "128x128_w4", "128x128_w4_s4", "192x256_w4", "256x192_w4", "256x256_pp",
+            "64x128_w4", "64x128_w4_s4"]
 TILES_NN = ["256x256_w4", "256x128_w4", "256x192_w4"]
 
 
