@@ -14,14 +14,14 @@ namespace dg {
 namespace {
 
 // The block kernels and the skinny kernel over the groups' tiles.
-template <class Op, int BP, int BQ, bool KT, bool GA>
+template <class Op, int BP, int BQ, int NS, bool KT, bool GA>
 __global__ void __launch_bounds__(256)
-__attribute__((amdgpu_waves_per_eu(TnCfg<Op, false, BP, BQ, 2>::WPE, TnCfg<Op, false, BP, BQ, 2>::WPE)))
+__attribute__((amdgpu_waves_per_eu(TnCfg<Op, false, BP, BQ, NS>::WPE, TnCfg<Op, false, BP, BQ, NS>::WPE)))
 grouped_kernel(const GroupedArgs A) {
   GemmArgs g;
   Gather gt;
   if (!group_tile<BP, BQ, Op::OE>(A, &g, &gt)) return;
-  gemm_tn_body<Op, false, BP, BQ, 2, KT, OneTile, GA>(g, OneTile{}, gt);
+  gemm_tn_body<Op, false, BP, BQ, NS, KT, OneTile, GA>(g, OneTile{}, gt);
 }
 
 template <class Op, bool KT, bool GA>
@@ -41,11 +41,11 @@ __global__ void __launch_bounds__(512) grouped_skinny(const GroupedArgs A) {
   gemm_i8_skinny_body<Op, SF, FF, 8, D, false, GA>(g, gt);
 }
 
-template <class Op, int BP, int BQ, bool GA>
+template <class Op, int BP, int BQ, int NS, bool GA>
 Launch four_wave(const char* name, bool kt) {
-  using Cfg = TnCfg<Op, false, BP, BQ, 2>;
-  return Launch{kt ? (const void*)&grouped_kernel<Op, BP, BQ, true, GA>
-                   : (const void*)&grouped_kernel<Op, BP, BQ, false, GA>,
+  using Cfg = TnCfg<Op, false, BP, BQ, NS>;
+  return Launch{kt ? (const void*)&grouped_kernel<Op, BP, BQ, NS, true, GA>
+                   : (const void*)&grouped_kernel<Op, BP, BQ, NS, false, GA>,
                 name, BP, BQ, Cfg::NT, Cfg::LDS, false};
 }
 
@@ -55,8 +55,9 @@ Launch skinny(const char* name) {
   return Launch{(const void*)&grouped_skinny<Op, SF, FF, 1, GA>, name, Cfg::SR, Cfg::FR, Cfg::NT, Cfg::LDS, false};
 }
 
-enum Kind { kPingPong, kFourWave, kSkinny16, kSkinny32, kSkinny64, kKinds };
-const char* const kNames[kKinds] = {"i8_grouped_256x256_pp", "i8_grouped_128x128_w4", "i8_grouped_skinny16",
+enum Kind { kPingPong, kFourWave, kFourStages, kNarrow, kSkinny16, kSkinny32, kSkinny64, kKinds };
+const char* const kNames[kKinds] = {"i8_grouped_256x256_pp", "i8_grouped_128x128_w4", "i8_grouped_128x128_w4_s4",
+                                    "i8_grouped_128x64_w4_s4", "i8_grouped_skinny16",
                                     "i8_grouped_skinny32", "i8_grouped_skinny64"};
 
 template <class Op, bool GA>
@@ -67,7 +68,9 @@ Launch launch_of(int kind, bool kt) {
       return Launch{kt ? (const void*)&grouped_pp<Op, true, GA> : (const void*)&grouped_pp<Op, false, GA>,
                     kNames[kind], 256, 256, Cfg::NT, Cfg::LDS, false};
     }
-    case kFourWave: return four_wave<Op, 128, 128, GA>(kNames[kind], kt);
+    case kFourWave: return four_wave<Op, 128, 128, 2, GA>(kNames[kind], kt);
+    case kFourStages: return four_wave<Op, 128, 128, 4, GA>(kNames[kind], kt);
+    case kNarrow: return four_wave<Op, 128, 64, 4, GA>(kNames[kind], kt);
     case kSkinny16: return skinny<Op, 2, 1, GA>(kNames[kind]);
     case kSkinny32: return skinny<Op, 2, 2, GA>(kNames[kind]);
     default: return skinny<Op, 2, 4, GA>(kNames[kind]);
@@ -87,19 +90,22 @@ Launch launch_for(int c_type, int kind, bool kt) {
 // device knows: every group that can have rows is taken to have some, with a
 // part-filled last tile half the time.  Estimated time in us: the larger of
 // what the kernel's tiles cost and of what reading the groups' weights costs it,
-//   256 x 256 (ping-pong, one per CU)   a round 13 us and 10.25 ns per k; weights at 3.8 TB/s
-//   128 x 128 (four waves, two per CU)  a round 10 us and 7.7 ns per k; weights at 4.1 TB/s
+//   256 x 256 (ping-pong, one per CU)   a round 13 us and 10.25 ns per k; weights at 4.0 TB/s
+//   128 x 128 (two stages, two per CU)  a round 10 us and 7.7 ns per k; weights at 3.9 TB/s
+//   128 x 128 (four stages, one)        a round 10 us and 6.4 ns per k; weights at 4.9 TB/s
+//   128 x 64 (four stages, one)         a round 7 us and 3.7 ns per k; weights at 4.3 TB/s
 //   skinny                              40 GB/s per CU of (32 + few) rows; weights at 4.9 TB/s
-// Measured (us; 256 x 256 / 128 x 128 / skinny of 16 / of 32), rows read
-// through an index, sizes uneven as a router's:
-//   128 rows, 64 groups, N 2048, K 4096     99 /  83 /   56 /   64
-//   512                                    124 / 114 /   86 /   97
-//   2048                                   147 / 156 /  164 /  154
-//   8192                                   181 / 178 /  421 /  345
-//   512 rows, 8 groups, N 4096, K 14336    152 / 126 /  208 /  159
-//   2006                                   169 / 261 /  623 /  490
-//   4096                                   308 / 361 / 1228 /  970
-//   32768 rows, 32 groups, N 4096, K 4096  518 / 707 / 2802 / 2064
+// Measured (us; 256 x 256 / 128 x 128 / the same with four stages / 128 x 64 /
+// skinny of 16 / of 32), sizes uneven as a router's:
+//   512 rows, 64 groups, N 2048, K 4096    123 / 114 / 129 / 115 /   87 /   97
+//   1024                                   136 / 130 / 137 / 120 /  121 /  122
+//   2048                                   143 / 157 / 152 / 131 /  164 /  155
+//   8192                                   179 / 180 / 207 / 215 /  420 /  347
+//   256 rows, 8 groups, N 4096, K 14336    145 / 118 /  95 / 126 /  131 /  108
+//   512                                    152 / 126 / 101 / 129 /  207 /  158
+//   1024                                   156 / 157 / 170 / 182 /  369 /  270
+//   2006                                   169 / 261 (four stages and narrow not measured)
+//   32768 rows, 32 groups, N 4096, K 4096  518 / 707
 int choose_kind(int64_t groups, int64_t rows, int64_t N, int64_t K) {
   const double cus = 256.0;
   const double some = (double)(groups < rows ? groups : rows);
@@ -113,8 +119,10 @@ int choose_kind(int64_t groups, int64_t rows, int64_t N, int64_t K) {
   };
   auto larger = [](double x, double y) { return x > y ? x : y; };
   double t[kKinds];
-  t[kPingPong] = larger(rounds(256, 256, 1) * (13.0 + (double)K * 10.25e-3), weights / 3.8e6);
-  t[kFourWave] = larger(rounds(128, 128, 2) * (10.0 + (double)K * 7.7e-3), weights / 4.1e6);
+  t[kPingPong] = larger(rounds(256, 256, 1) * (13.0 + (double)K * 10.25e-3), weights / 4.0e6);
+  t[kFourWave] = larger(rounds(128, 128, 2) * (10.0 + (double)K * 7.7e-3), weights / 3.9e6);
+  t[kFourStages] = larger(rounds(128, 128, 1) * (10.0 + (double)K * 6.4e-3), weights / 4.9e6);
+  t[kNarrow] = larger(rounds(128, 64, 1) * (7.0 + (double)K * 3.7e-3), weights / 4.3e6);
   for (int kind = kSkinny16; kind <= kSkinny64; ++kind) {
     const int few = 16 << (kind - kSkinny16);
     const double wgs = tiles(few) * (double)((N + 31) / 32) / cus;

@@ -407,7 +407,7 @@ def test_grouped_larger(counts, N, K, gather):
 
 
 @pytest.mark.parametrize("gather", [False, True], ids=["sorted", "gather"])
-@pytest.mark.parametrize("kernel", ["256x256_pp", "128x128_w4", "skinny16", "skinny32", "skinny64"])
+@pytest.mark.parametrize("kernel", ["256x256_pp", "128x128_w4", "128x128_w4_s4", "128x64_w4_s4", "skinny16", "skinny32", "skinny64"])
 def test_grouped_every_kernel(monkeypatch, kernel, gather):
     """Each kernel a grouped product can take, on groups below, at and past its
     tile, K from below a stage to several, whole and ending inside a chunk."""
