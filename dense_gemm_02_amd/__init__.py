@@ -1,5 +1,6 @@
 """MI355X (gfx950) tiled dense GEMM: C = A x B in FP32, FP16, BF16 and FP8 E4M3
-with FP32 accumulation, behind the C-ABI library ``libdgemm.so``.
+with FP32 accumulation, int8 linear layers and mixtures of experts, behind the
+C-ABI library ``libdgemm.so``.
 
 The compute path is hand-written HIP in ``csrc/``; this package only marshals
 arguments to it (``dense_gemm_02_amd.binding``).  Importing the package does

@@ -12,35 +12,45 @@ from __future__ import annotations
 
 import functools
 
-from .binding import DgemmError, _device_tensors, _factor_vector, _need, load_library
+from .binding import DgemmError, _factor_vector, _need, load_library
 
-_TYPES = None
+# What a call needs of torch and the library, looked up once: on a small call
+# the lookups would cost as much as its launch.
+_TYPES = {}
+_calls = {}
+_raw_stream = _current_device = None
 
 
 def type_code(dtype):
     """The dgemm_type of a torch dtype."""
-    global _TYPES
-    if _TYPES is None:
+    if not _TYPES:
         import torch
-        _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+        _TYPES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
     code = _TYPES.get(dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {dtype}: float32, float16 or bfloat16")
     return code
 
 
+def _entry(name):
+    global _raw_stream, _current_device
+    import torch
+    # (The raw handle: building a Stream object alone takes 1.7 us.)
+    _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _calls[name] = getattr(load_library(), name)
+    return _calls[name]
+
+
 def call(name, device, *args):
     """One library call on the current stream of `device`, with it current."""
-    import torch
-    # (The raw handle: building a Stream object costs as much as the rest of a
-    # small call, 1.7 us.)
-    handle = torch._C._cuda_getCurrentRawStream(device.index)
-    fn = getattr(load_library(), name)
-    if device.index == torch._C._cuda_getDevice():
-        st = fn(*args, handle)
+    fn = _calls.get(name) or _entry(name)
+    index = device.index
+    if index == _current_device():
+        st = fn(*args, _raw_stream(index))
     else:
+        import torch
         with torch.cuda.device(device):
-            st = fn(*args, handle)
+            st = fn(*args, _raw_stream(index))
     if st != 0:
         raise DgemmError(st, name)
 
@@ -66,11 +76,16 @@ def takes_stream(fn):
 
 def one_device(names, first, *rest):
     """All of them device tensors of one device (None: not given)."""
-    _device_tensors(names, first, *(t for t in rest if t is not None))
+    if not getattr(first, "is_cuda", False):
+        raise TypeError(f"{names} must be device tensors")
+    device = first.device
     for t in rest:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{names} must be on one device")
-    return first.device
+        if t is not None:
+            if not getattr(t, "is_cuda", False):
+                raise TypeError(f"{names} must be device tensors")
+            if t.device != device:
+                raise ValueError(f"{names} must be on one device")
+    return device
 
 
 def pitch(t, what, align=1):
