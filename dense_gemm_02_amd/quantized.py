@@ -175,11 +175,13 @@ def matmul_i8(a, b, scale_a, scale_b, out=None, out_dtype=None):
     odt = out_dtype or (out.dtype if out is not None else torch.float32)
     code = type_code(odt)
     if out is None:
-        out = (torch.empty((M, N), dtype=odt, device=device) if layout == 0
-               else torch.empty((N, M), dtype=odt, device=device).t())
-    if out.shape != (M, N) or out.dtype != odt:
+        # (One allocation: .t() of a new tensor, and of out for its pitch, cost 1 us each.)
+        ldc = max(N if layout == 0 else M, 1)
+        out = torch.empty_strided((M, N), (ldc, 1) if layout == 0 else (1, ldc), dtype=odt, device=device)
+    elif out.shape != (M, N) or out.dtype != odt:
         raise ValueError("out must be a device tensor of shape (M, N) and the output dtype")
-    ldc = pitch(out if layout == 0 else out.t(), "out (NN) or its transpose (TN)")
+    else:
+        ldc = pitch(out if layout == 0 else out.t(), "out (NN) or its transpose (TN)")
     _factor_vector(scale_a, M, "scale_a")
     _factor_vector(scale_b, N, "scale_b")
     if M > 0 and N > 0 and K > 0:
