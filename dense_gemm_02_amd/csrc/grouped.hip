@@ -90,11 +90,11 @@ Launch launch_for(int c_type, int kind, bool kt) {
 // device knows: every group that can have rows is taken to have some, with a
 // part-filled last tile half the time.  Estimated time in us: the larger of
 // what the kernel's tiles cost and of what reading the groups' weights costs it,
-//   256 x 256 (ping-pong, one per CU)   a round 13 us and 10.25 ns per k; weights at 4.0 TB/s
-//   128 x 128 (two stages, two per CU)  a round 10 us and 7.7 ns per k; weights at 3.9 TB/s
-//   128 x 128 (four stages, one)        a round 10 us and 6.4 ns per k; weights at 4.9 TB/s
-//   128 x 64 (four stages, one)         a round 7 us and 3.7 ns per k; weights at 4.3 TB/s
-//   skinny                              40 GB/s per CU of (32 + few) rows; weights at 4.9 TB/s
+//   256 x 256 (ping-pong, one per CU)   a round 12.5 us and 10.25 ns per k; weights at 4.0 TB/s
+//   128 x 128 (two stages, two per CU)  a round 8.3 us and 7.7 ns per k; weights at 3.9 TB/s
+//   128 x 128 (four stages, one)        a round 8 us and 6.4 ns per k; weights at 4.9 TB/s
+//   128 x 64 (four stages, one)         a round 5.3 us and 3.7 ns per k; weights at 4.3 TB/s
+//   skinny of `few` rows                a tile 54 ns * few and (32 + few) * K at 40 GB/s per CU; weights at 4.9 TB/s
 // Measured (us; 256 x 256 / 128 x 128 / the same with four stages / 128 x 64 /
 // skinny of 16 / of 32), sizes uneven as a router's:
 //   512 rows, 64 groups, N 2048, K 4096    123 / 114 / 129 / 115 /   87 /   97
@@ -106,6 +106,11 @@ Launch launch_for(int c_type, int kind, bool kt) {
 //   1024                                   156 / 157 / 170 / 182 /  369 /  270
 //   2006                                   169 / 261 (four stages and narrow not measured)
 //   32768 rows, 32 groups, N 4096, K 4096  518 / 707
+//   30788 rows, 5 groups, N 2990, K 68      76 / 100 / 187 / 250 /  753 /  599
+//   30788 rows, 5 groups, N 2990, K 1024   127 / 159 / 292 / 376 / 1014 /  758
+//   12054 rows, 79 groups, N 1021, K 445    41 /  37 /  57 /  64 /  184 /  133
+//   4096 rows, 8 groups, N 4096, K 128      16 /  20 /  34 /  43 /  140 /  109
+//   512 rows, 64 groups, N 2048, K 256      22 /  14 /  24 /  21 /   23 /   32
 int choose_kind(int64_t groups, int64_t rows, int64_t N, int64_t K) {
   const double cus = 256.0;
   const double some = (double)(groups < rows ? groups : rows);
@@ -119,14 +124,14 @@ int choose_kind(int64_t groups, int64_t rows, int64_t N, int64_t K) {
   };
   auto larger = [](double x, double y) { return x > y ? x : y; };
   double t[kKinds];
-  t[kPingPong] = larger(rounds(256, 256, 1) * (13.0 + (double)K * 10.25e-3), weights / 4.0e6);
-  t[kFourWave] = larger(rounds(128, 128, 2) * (10.0 + (double)K * 7.7e-3), weights / 3.9e6);
-  t[kFourStages] = larger(rounds(128, 128, 1) * (10.0 + (double)K * 6.4e-3), weights / 4.9e6);
-  t[kNarrow] = larger(rounds(128, 64, 1) * (7.0 + (double)K * 3.7e-3), weights / 4.3e6);
+  t[kPingPong] = larger(rounds(256, 256, 1) * (12.5 + (double)K * 10.25e-3), weights / 4.0e6);
+  t[kFourWave] = larger(rounds(128, 128, 2) * (8.3 + (double)K * 7.7e-3), weights / 3.9e6);
+  t[kFourStages] = larger(rounds(128, 128, 1) * (8.0 + (double)K * 6.4e-3), weights / 4.9e6);
+  t[kNarrow] = larger(rounds(128, 64, 1) * (5.3 + (double)K * 3.7e-3), weights / 4.3e6);
   for (int kind = kSkinny16; kind <= kSkinny64; ++kind) {
     const int few = 16 << (kind - kSkinny16);
     const double wgs = tiles(few) * (double)((N + 31) / 32) / cus;
-    t[kind] = larger((wgs > 1 ? wgs : 1) * (32 + few) * (double)K / 40e3, weights / 4.9e6);
+    t[kind] = larger((wgs > 1 ? wgs : 1) * ((32 + few) * (double)K / 40e3 + 0.054 * few), weights / 4.9e6);
   }
   // (Sweeps and tests: DGEMM_CONFIG=<kernel name> forces a kernel, as for gemm_*.)
   if (const char* want = getenv("DGEMM_CONFIG"))
@@ -187,8 +192,6 @@ extern "C" int gemm_i8_grouped(int64_t groups, int64_t rows, int64_t N, int64_t 
   g.Q = (const char*)A; g.ldq = lda; g.Qn = rows;
   g.C = C; g.ldc = ldc; g.K = K;
   g.group = 8;
-  g.vec_store = aligned(C, 4 * oe) && ldc % 4 == 0;
-  g.vec16 = aligned(C, 16) && ldc % (16 / oe) == 0;
   g.sp = scale_b; g.sp_row = n_scale_b > 1 ? 1 : 0;
   g.sq = scale_a; g.sq_row = n_scale_a > 1 ? 1 : 0;
   a.offsets = offsets; a.groups = groups; a.rows = rows; a.pstride = group_b;
