@@ -426,6 +426,42 @@ def test_grouped_every_kernel(monkeypatch, kernel, gather):
                 near(got[written], want[written])
 
 
+@pytest.mark.parametrize("layout,tile", [("tn", t) for t in TILES_TN + ["skinny"]] + [("nn", t) for t in TILES_NN])
+@pytest.mark.parametrize("tag,dtype", [("i8f", torch.float32), ("i8h", torch.float16), ("i8b", torch.bfloat16)])
+def test_every_kernel_stores_at_any_alignment(monkeypatch, layout, tile, tag, dtype):
+    """Rows of results at every offset of a 16-byte grid, of odd and even
+    pitches; what lies before and behind them stays."""
+    if tile != "skinny":
+        monkeypatch.setenv("DGEMM_CONFIG", f"{tag}_{layout}_{tile}")
+    M, N = (300, 17) if tile == "skinny" else (303, 290)
+    a, b, sa, sb = operands(layout, M, N, 272, 9)
+    want = exact(a, b, sa, sb)
+    rows, n = (N, M) if layout == "tn" else (M, N)
+    for off in range(16 // dtype.itemsize + 1):
+        for extra in (9, 10, 16):
+            print(f"{tag} {layout} {tile} offset {off} pitch {n + extra}", flush=True)
+            wide = torch.full((rows, n + extra), 7.0, device="cuda").to(dtype)
+            part = wide[:, off:off + n]
+            near(lib().matmul(a, b, scale_a=sa, scale_b=sb, out=part.t() if layout == "tn" else part), want)
+            assert (wide[:, :off] == 7).all() and (wide[:, off + n:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("kernel", ["256x256_pp", "128x128_w4", "128x128_w4_s4", "128x64_w4_s4", "skinny16", "skinny32", "skinny64"])
+def test_grouped_stores_at_any_alignment(monkeypatch, kernel, dtype):
+    monkeypatch.setenv("DGEMM_CONFIG", "i8_grouped_" + kernel)
+    c = grouped_case([70, 0, 3, 260], 141, 200, 17, False, tail=3, lead=2)
+    want = grouped_exact(*c)
+    written = ~torch.isnan(want[:, 0])
+    for off in range(16 // dtype.itemsize + 1):
+        for extra in (9, 10, 16):
+            print(f"grouped {kernel} {dtype} offset {off} pitch {141 + extra}", flush=True)
+            wide = torch.full((c[6], 141 + extra), 7.0, device="cuda").to(dtype)
+            got = lib().matmul_grouped(*c[:5], out=wide[:, off:off + 141])
+            near(got[written], want[written])
+            assert (got[~written] == 7).all() and (wide[:, :off] == 7).all() and (wide[:, off + 141:] == 7).all()
+
+
 def test_grouped_indexes_without_a_row():
     """Indexes outside a count as zeros with the factor 0; the same row many
     times; an a with no rows."""
