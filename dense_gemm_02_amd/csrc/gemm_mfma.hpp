@@ -300,6 +300,31 @@ struct EpiScale {
       r[e] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rp, (int)((p + e) * 4), 0, 0));
     return r;
   }
+  // The factors of all of a lane's groups of four p at once (ANY_AT kernels):
+  // one wait, not one a group.  With the batched stores of staged_epilogue,
+  // us: 8192^3 385 -> 377, 32768 rows of 32 experts 507 -> 494, 30788 rows
+  // of 5 with K 68 76 -> 71.  (The direct epilogue gained nothing by it:
+  // 2047 x 4099 x 4111 NN 65 and 66.)
+  template <int TP, int NG>
+  __device__ static void all_p(const GemmArgs& a, int64_t p, f32x4 (&f)[TP][NG]) {
+    if (!a.sp_row) {
+      const float one = a.sp[0];
+#pragma unroll
+      for (int i = 0; i < TP; ++i)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) f[i][g] = f32x4{one, one, one, one};
+      return;
+    }
+    const __amdgpu_buffer_rsrc_t rp = make_rsrc(a.sp, (uint32_t)(a.Pn * 4));
+#pragma unroll
+    for (int i = 0; i < TP; ++i)
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          f[i][g][e] = __builtin_bit_cast(
+              float, __builtin_amdgcn_raw_buffer_load_b32(rp, (int)((p + MT * i + 8 * g + e) * 4), 0, 0));
+  }
   __device__ void apply(const f32x4& fp, int j, float& v0, float& v1, float& v2, float& v3) const {
     v0 *= fp[0] * fq[j];
     v1 *= fp[1] * fq[j];
@@ -343,6 +368,8 @@ __device__ __forceinline__ void staged_epilogue(const GemmArgs& a, char* reg, co
   const int lr = lane % MT, lg = lane / MT;
   [[maybe_unused]] EpiScale<TQ, MT, GA> sc;
   if constexpr (Op::SCALED) sc.init(a, lane, qbase, gt);
+  [[maybe_unused]] f32x4 fpa[TP][NG];
+  if constexpr (Op::ANY_AT) EpiScale<TQ, MT, GA>::template all_p<TP, NG>(a, pbase + 4 * lg, fpa);
 #pragma unroll
   for (int pass = 0; pass < PASSES; ++pass) {
 #pragma unroll
@@ -350,7 +377,8 @@ __device__ __forceinline__ void staged_epilogue(const GemmArgs& a, char* reg, co
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         [[maybe_unused]] f32x4 fp;
-        if constexpr (Op::SCALED) fp = EpiScale<TQ, MT, GA>::p4(a, pbase + MT * (pass * TPP + i) + 8 * g + 4 * lg);
+        if constexpr (Op::ANY_AT) fp = fpa[pass * TPP + i][g];
+        else if constexpr (Op::SCALED) fp = EpiScale<TQ, MT, GA>::p4(a, pbase + MT * (pass * TPP + i) + 8 * g + 4 * lg);
 #pragma unroll
         for (int j = 0; j < TQ; ++j) {
           const AccT& v = acc[pass * TPP + i][j];
@@ -373,6 +401,35 @@ __device__ __forceinline__ void staged_epilogue(const GemmArgs& a, char* reg, co
         }
       }
     const int m = lane & 15;                  // 16-byte chunk within a row
+    if constexpr (Op::ANY_AT) {
+      // Every p inside: eight reads in flight, then their stores, where the
+      // loop below waits for each read before its store.
+      const int64_t p0 = pbase + pass * TPP * MT;
+      if (p0 + TPP * MT <= a.Pn) {
+        constexpr int B = WTQ / 4 < 8 ? WTQ / 4 : 8;
+        static_assert(WTQ / 4 % B == 0, "whole batches");
+#pragma unroll
+        for (int b = 0; b < WTQ / 4; b += B) {
+          u32x4 d[B];
+#pragma unroll
+          for (int it = 0; it < B; ++it) {
+            const int row = 4 * (b + it) + (lane >> 4), kr = key(row);
+            if constexpr (OE == 4) {
+              d[it] = *(const u32x4*)(reg + row * RB + ((m ^ kr) * 16));
+            } else {
+              const u32x4 raw = *(const u32x4*)(reg + row * RB + ((((2 * m) ^ kr) & ~1) * SS));
+              d[it] = (kr & 1) ? u32x4{raw[2], raw[3], raw[0], raw[1]} : raw;
+            }
+          }
+#pragma unroll
+          for (int it = 0; it < B; ++it) {
+            const int64_t q = qbase + 4 * (b + it) + (lane >> 4);
+            if (q < a.Qn) *(u32x4_at2*)((char*)a.C + (q * a.ldc + p0 + m * EPC) * OE) = d[it];
+          }
+        }
+        continue;
+      }
+    }
 #pragma unroll
     for (int it = 0; it < WTQ / 4; ++it) {
       const int row = 4 * it + (lane >> 4);
