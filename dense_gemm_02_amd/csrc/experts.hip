@@ -457,7 +457,9 @@ int expert_combine_grad(int64_t tokens, int64_t k, int64_t H, int type, const vo
       !aligned_to(weights, 4) || !aligned_to(dW, 4))
     return DGEMM_ERR_MISALIGNED;
   if (too_many(tokens, k, rows, H)) return DGEMM_ERR_UNSUPPORTED;
-  RowArgs a{dO, ldo, Y, ldy, dY, lddy, slot, weights, dW, tokens, k, H, rows};
+  // No sorted rows: every pair is dropped and dW is zeros.  dO may be NULL then,
+  // so the kernel is given rows of no elements (it loads dO whatever the slots are).
+  RowArgs a{dO, ldo, Y, ldy, dY, lddy, slot, weights, dW, tokens, k, some ? H : 0, rows};
   return launch_rows(kCombineGrad, type, a, stream);
 }
 

@@ -238,7 +238,8 @@ int quantize_i8(int64_t rows, int64_t K, const void* X, int64_t ldx, int x_type,
  *   dY[slot[t*k + j]] = w[t*k + j] * dO[t],  dW[t*k + j] = dO[t] . Y[slot[t*k + j]]
  * (FP32, 0 for a dropped pair); rows of dY that no slot names are left.
  * weights == NULL: all 1; dW == NULL: not wanted (Y is then not read and may
- * be NULL); dY == NULL likewise.
+ * be NULL); dY == NULL likewise.  With rows == 0 or H == 0 neither dO nor Y is
+ * read (both may be NULL) and dW is zeros.
  * What a call writes must not overlap what it reads.
  * In all three a slot outside 0 .. rows - 1 (rows: of Y and dY) counts as
  * dropped; a slot must not occur twice where rows are written.  `type` is the
