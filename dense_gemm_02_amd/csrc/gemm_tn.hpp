@@ -171,7 +171,11 @@ __device__ __forceinline__ void gemm_tn_body(const GemmArgs& a, TileOf tile_of, 
       const int kr = Cfg::RPSG * (i * NW + wave_u) + (lane * 16) / Cfg::PROWB;
       const int br = (lane * 16) % Cfg::PROWB;
       const int lu = (br / Cfg::UB) ^ Cfg::pkey(kr);
-      pvo[i] = (uint32_t)(kr * a.ldp + lu * Cfg::UB + br % Cfg::UB);
+      const int64_t at = kr * a.ldp + lu * Cfg::UB + br % Cfg::UB;
+      // Int8 takes any K, so ld may be near 2^31 and a row past K's offset at
+      // or past 2^32: it has to stay out of range, not wrap around into it.
+      // (The other formats have K above the rows of a stage: at < 2^31.)
+      pvo[i] = Op::TRIM && at >= (int64_t)kOobOffset ? kOobOffset : (uint32_t)at;
     }
   }
   // Copy source of one tile: block base pointers and descriptor sizes.  A

@@ -32,3 +32,30 @@ def test_combine_grad_without_sorted_rows(dtype):
         dw = torch.full((T * k + 1,), 7.0, device="cuda")
         assert grad(T, k, H, dtype, None, H, None, 0, H, slot.data_ptr(), None, None, H, dw.data_ptr(), stream) == 0
         assert (dw[:-1] == 0).all() and dw[-1] == 7
+
+
+@pytest.mark.parametrize("K,ldb", [(1, 2 ** 31 - 64), (2, 2 ** 30 - 32), (3, 2 ** 29), (5, 2 ** 28 + 2 ** 27),
+                                   (7, 2 ** 28 + 2 ** 25)])
+@pytest.mark.parametrize("tile", [None, "256x256_w4", "256x128_w4", "256x192_w4"])
+def test_row_major_b_of_the_longest_pitch(monkeypatch, tile, K, ldb):
+    """K * ldb at its limit with a few rows of B: what A holds behind K (other
+    values here) meets nothing, whichever kernel runs.  Rows of B are of the
+    values' full range on both sides of the N columns that count."""
+    import ctypes
+    L = lib()
+    M, N = (4096, 4096) if tile is None else (300, 333)
+    if tile is not None:
+        monkeypatch.setenv("DGEMM_CONFIG", f"i8f_nn_{tile}")
+    buf = ctypes.create_string_buffer(256)
+    assert L.load_library().dgemm_kernel_config(6, 0, M, N, K, buf, 256) == 0
+    assert buf.value.decode().startswith("i8f_nn_" + (tile or "256x256_w4")), buf.value
+    print(f"K={K} ldb={ldb} {buf.value.decode()}", flush=True)
+    g = gen(K)
+    A = torch.randint(-128, 128, (M, 16), generator=g, device="cuda", dtype=torch.int8)
+    B = torch.full((K, ldb), 77, device="cuda", dtype=torch.int8)
+    B[:, :N] = torch.randint(-128, 128, (K, N), generator=g, device="cuda", dtype=torch.int8)
+    C = torch.empty((M, N), device="cuda")
+    one = torch.ones(1, device="cuda")
+    L.gemm_i8("nn", M, N, K, A, 16, B, ldb, C, N, one, one)
+    # sums of at most 7 * 2^14: exact in FP32
+    assert torch.equal(C.double(), A[:, :K].double() @ B[:, :N].double())
