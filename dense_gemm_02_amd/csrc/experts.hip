@@ -359,7 +359,20 @@ int launch_rows(RowOp op, int type, RowArgs a, void* stream) {
     if (stream_rows) return one ? row_kernel<T, true, 1>(op) : row_kernel<T, true, 4>(op);
     return one ? row_kernel<T, false, 1>(op) : row_kernel<T, false, 4>(op);
   });
-  return launch_kernel(fn, one ? (a.tokens + 3) / 4 : a.tokens, 256, &a, stream);
+  const int64_t per = one ? 4 : 1, step = kMaxRowBlocks * per;
+  for (int64_t at = 0; at < a.tokens; at += step) {
+    // Tokens at .. of the matrices by token and of the slots and weights; the
+    // sorted rows stay whole.
+    RowArgs part = a;
+    part.tokens = a.tokens - at < step ? a.tokens - at : step;
+    if (a.x != nullptr) part.x = (const char*)a.x + at * a.ldx * e;
+    if (op == kCombine) part.out = (char*)a.out + at * a.ldo * e;
+    if (a.slot != nullptr) part.slot = a.slot + at * a.k;
+    if (a.w != nullptr) part.w = a.w + at * a.k;
+    if (a.dw != nullptr) part.dw = a.dw + at * a.k;
+    if (const int st = launch_kernel(fn, (part.tokens + per - 1) / per, 256, &part, stream)) return st;
+  }
+  return DGEMM_OK;
 }
 
 // The checks the three row operators share, up to the limits.

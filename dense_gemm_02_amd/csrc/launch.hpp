@@ -62,6 +62,11 @@ constexpr int64_t kMaxDescBytes = (int64_t(1) << 31) - 64;
 // The sum of K products of two int8 values fits 32 bits up to this K.
 constexpr int64_t kMaxI8K = 131071;
 
+// The row operators' launches have at most this many workgroups, and more rows
+// take several: HIP takes fewer than 2^32 work-items a launch, which 1024
+// threads a row would reach at 2^22 rows.
+constexpr int64_t kMaxRowBlocks = int64_t(1) << 21;
+
 // One launch on the caller's stream.
 inline int launch_kernel(const void* fn, int64_t grid, int threads, void* arg, void* stream) {
   void* args[] = {arg};

@@ -235,5 +235,18 @@ extern "C" int quantize_i8(int64_t rows, int64_t K, const void* X, int64_t ldx, 
     using T = decltype(t);
     return stream_rows ? quantize_choice<T, true>(K, &per) : quantize_choice<T, false>(K, &per);
   });
-  return launch_kernel(fn, per > 0 ? (rows + per - 1) / per : rows, per > 0 ? 256 : 1024, &a, stream);
+  const int threads = per > 0 ? 256 : 1024;
+  if (per == 0) per = 1;
+  const int64_t step = kMaxRowBlocks * per;
+  for (int64_t at = 0; at < rows; at += step) {
+    QuantArgs part = a;
+    if (K > 0) {   // (else both may be null)
+      part.X = (const char*)X + at * ldx * type_bytes(x_type);
+      part.Q = Q + at * ldq;
+    }
+    part.scale = scale + at;
+    part.rows = rows - at < step ? rows - at : step;
+    if (const int st = launch_kernel(fn, (part.rows + per - 1) / per, threads, &part, stream)) return st;
+  }
+  return DGEMM_OK;
 }

@@ -59,3 +59,71 @@ def test_row_major_b_of_the_longest_pitch(monkeypatch, tile, K, ldb):
     L.gemm_i8("nn", M, N, K, A, 16, B, ldb, C, N, one, one)
     # sums of at most 7 * 2^14: exact in FP32
     assert torch.equal(C.double(), A[:, :K].double() @ B[:, :N].double())
+
+
+# ---- more rows than one launch holds ------------------------------------------------
+# (A workgroup of 256 threads a row is 2^32 work-items at 2^24 rows, of four
+# rows at 2^26; the matrices repeat every 251 rows, so that all of a result can
+# be compared with its first rows.)
+
+PERIOD = 251
+
+
+def check_repeats(t, name):
+    """t's rows repeat those of its first PERIOD."""
+    step = PERIOD * max(1, 2 ** 28 // (PERIOD * max(1, t[0].numel())))
+    first = t[:PERIOD].repeat((step // PERIOD,) + (1,) * (t.dim() - 1))
+    for r in range(0, t.shape[0], step):
+        part = t[r:r + step]
+        assert torch.equal(part, first[:part.shape[0]]), (name, r)
+
+
+def repeating(rows, H, dtype, seed, pitch=None):
+    first = torch.randn((PERIOD, H), generator=gen(seed), device="cuda").to(dtype)
+    x = torch.empty((rows, pitch or H), dtype=dtype, device="cuda")[:, :H]
+    n = rows // PERIOD * PERIOD
+    x[:n].unflatten(0, (-1, PERIOD)).copy_(first.expand(n // PERIOD, PERIOD, H))
+    x[n:] = first[:rows - n]
+    return x
+
+
+@pytest.mark.parametrize("rows,K,dtype", [(2 ** 26 + 5, 3, torch.float32), (2 ** 24 + 3, 1025, torch.bfloat16),
+                                          (2 ** 21 + 5, 16385, torch.float16)])
+def test_quantize_more_rows_than_a_launch(rows, K, dtype):
+    """One wave a row, one workgroup a row, and the rows of two passes."""
+    print(f"quantize {rows}x{K} {dtype}", flush=True)
+    x = repeating(rows, K, dtype, 1)
+    q, s = lib().quantize_i8(x)
+    s0 = (x[:PERIOD].double().abs().amax(1) / 127).float()
+    q0 = torch.round(x[:PERIOD].double() / s0.double()[:, None]).to(torch.int8)
+    assert torch.equal(s[:PERIOD], s0) and torch.equal(q[:PERIOD], q0)
+    check_repeats(s, "scale")
+    check_repeats(q, "q")
+
+
+@pytest.mark.parametrize("T,H,dtype", [(2 ** 26 + 5, 5, torch.float16), (2 ** 24 + 3, 520, torch.bfloat16)])
+def test_rows_of_more_tokens_than_a_launch(T, H, dtype):
+    """Two choices a token, the second dropped, and rows of one wave and of
+    one workgroup.  Weights are powers of two, so products round nothing."""
+    L = lib()
+    print(f"rows {T}x2 H={H} {dtype}", flush=True)
+    x = repeating(T, H, dtype, 2)
+    slot = torch.full((T, 2), -1, dtype=torch.int32, device="cuda")
+    slot[:, 0] = torch.arange(T, device="cuda", dtype=torch.int32)
+    w = torch.full((T, 2), float("nan"), device="cuda")
+    w[:, 0] = 2.0 ** ((torch.arange(T, device="cuda") % PERIOD) % 3 - 1).float()
+    y = L.expert_dispatch(x, slot, rows=T)
+    assert torch.equal(y[:PERIOD], x[:PERIOD])
+    check_repeats(y, "dispatch")
+    want = (x[:PERIOD].double() * w[:PERIOD, :1].double()).to(dtype)
+    out = L.expert_combine(y, slot, w)
+    assert torch.equal(out[:PERIOD], want)
+    check_repeats(out, "combine")
+    dy, dw = L.expert_combine_grad(x, y, slot, w, dy=out)
+    assert torch.equal(dy[:PERIOD], want)
+    check_repeats(dy, "dy")
+    d64 = (x[:PERIOD].double() ** 2).sum(1)
+    # a sum of H squares in FP32, in any order
+    assert ((dw[:PERIOD, 0].double() - d64).abs() <= H * 2.0 ** -24 * (1 + 2.0 ** -10) * d64).all()
+    assert (dw[:, 1] == 0).all()
+    check_repeats(dw, "dweights")
