@@ -477,14 +477,14 @@ int plan(int dt, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, co
     out->L2 = ch.T;
     out->g2 = g2;
     out->grid2 = g2.tiles_p * g2.tiles_q;
-    if (out->grid2 > 0x7fffffff) return DGEMM_ERR_UNSUPPORTED;
+    if (!launchable(out->grid2, ch.T.threads)) return DGEMM_ERR_UNSUPPORTED;
   }
   g.tiles_p = skinny ? 1 : (g.Pn + L.bp - 1) / L.bp;
   g.tiles_q = (g.Qn + L.bq - 1) / L.bq;
   out->L = L;
   out->g = g;
   out->grid = g.tiles_p * g.tiles_q;
-  if (out->grid > 0x7fffffff) return DGEMM_ERR_UNSUPPORTED;
+  if (!launchable(out->grid, L.threads)) return DGEMM_ERR_UNSUPPORTED;
   return DGEMM_OK;
 }
 

@@ -202,6 +202,6 @@ extern "C" int gemm_i8_grouped(int64_t groups, int64_t rows, int64_t N, int64_t 
   const int64_t some = groups < rows ? groups : rows;
   g.tiles_q = (rows + some * (L.bq - 1)) / L.bq;
   const int64_t grid = g.tiles_p * g.tiles_q;
-  if (grid > kMaxCount) return DGEMM_ERR_UNSUPPORTED;
+  if (!launchable(grid, L.threads)) return DGEMM_ERR_UNSUPPORTED;
   return launch_kernel(L.fn, grid, L.threads, &a, stream);
 }

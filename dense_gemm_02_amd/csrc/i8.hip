@@ -89,6 +89,7 @@ bool skinny_i8_tn(int out, int64_t Pn, int64_t Qn, int64_t K, Launch* L) {
   const double small = t64 <= kCus ? 185.0 : (t64 <= 2 * kCus ? 230.0 : 308.0 * ceil(t128 / (2 * kCus)));
   const double large = 410.0 * ceil(t256 / kCus);
   if (few > 32 && best > (small < large ? small : large)) return false;
+  if (!launchable((int64_t)wgs, 512)) return false;   // (2^28 rows of 16 bytes; the block tiles take these)
   const bool two = wgs <= kCus && K >= 2048;
   auto pick = [&](auto op) {
     using Op = decltype(op);

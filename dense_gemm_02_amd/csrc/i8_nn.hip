@@ -62,6 +62,7 @@ bool skinny_i8_nn(int out, int64_t Pn, int64_t Qn, Launch* L) {
   const double narrow = 497.0 * ceil(tiles(Pn, 256) * tiles(Qn, 128) / kCus);
   const double square = 760.0 * ceil(tiles(Pn, 256) * tiles(Qn, 256) / kCus);
   if (best > (narrow < square ? narrow : square)) return false;
+  if (!launchable(((Pn + sp - 1) / sp) * ((Qn + fr - 1) / fr), 512)) return false;   // (2^30 rows; as in TN)
   *L = out == DGEMM_F32 ? pick<OpI8F>(sp, fr) : (out == DGEMM_F16 ? pick<OpI8H>(sp, fr) : pick<OpI8B>(sp, fr));
   return true;
 }

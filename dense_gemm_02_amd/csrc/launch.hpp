@@ -62,9 +62,11 @@ constexpr int64_t kMaxDescBytes = (int64_t(1) << 31) - 64;
 // The sum of K products of two int8 values fits 32 bits up to this K.
 constexpr int64_t kMaxI8K = 131071;
 
+// HIP takes fewer than 2^32 work-items a launch.
+inline bool launchable(int64_t grid, int threads) { return grid <= 0xffffffffll / threads; }
+
 // The row operators' launches have at most this many workgroups, and more rows
-// take several: HIP takes fewer than 2^32 work-items a launch, which 1024
-// threads a row would reach at 2^22 rows.
+// take several (1024 threads a row would not be launchable from 2^22 rows on).
 constexpr int64_t kMaxRowBlocks = int64_t(1) << 21;
 
 // One launch on the caller's stream.

@@ -36,7 +36,10 @@
  * element alignment (wider stores are used when C and ldc allow them).
  * Size limits: the bytes one block tile addresses in an operand must stay
  * below 2^31 (for a K-contiguous operand: 256 rows * ld * elem; for the NN
- * B operand: K * ldb * elem); beyond that the call returns DGEMM_ERR_UNSUPPORTED.
+ * B operand: K * ldb * elem), and the tiles of C have to fit a launch (fewer
+ * than 2^32 work-items: they do while the product of M and N, both rounded up
+ * to multiples of 32, is below 2^32); beyond that the call returns
+ * DGEMM_ERR_UNSUPPORTED.
  *
  * Streams.  The work is enqueued on `stream` (a hipStream_t; NULL = the null
  * stream) and the call returns without synchronising.  Faults inside the
@@ -187,7 +190,9 @@ int gemm_i8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda
  * work; NULL pointers (A and B may be NULL if K == 0, A and scale_a if
  * rows_a == 0); leading dimensions; alignment; limits ->
  * DGEMM_ERR_UNSUPPORTED: K above 131071; 256*lda, 256*ldb, 4*rows, 4*rows_a,
- * 4*N or (with row_index) rows_a*lda at or above 2^31.
+ * 4*N or (with row_index) rows_a*lda at or above 2^31; more tiles than a launch
+ * holds (never while N, rounded up to a multiple of 32, times rows + 15*groups
+ * is below 2^32).
  */
 int gemm_i8_grouped(int64_t groups, int64_t rows, int64_t N, int64_t K, const int8_t* A, int64_t rows_a, int64_t lda,
                     const int32_t* row_index, const int8_t* B, int64_t ldb, int64_t group_b, void* C, int64_t ldc,

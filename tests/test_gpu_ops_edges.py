@@ -127,3 +127,25 @@ def test_rows_of_more_tokens_than_a_launch(T, H, dtype):
     assert ((dw[:PERIOD, 0].double() - d64).abs() <= H * 2.0 ** -24 * (1 + 2.0 ** -10) * d64).all()
     assert (dw[:, 1] == 0).all()
     check_repeats(dw, "dweights")
+
+
+@pytest.mark.parametrize("few", [1, 3])
+def test_product_of_more_strips_than_a_launch(few):
+    """2^28 rows of 16 bytes against a few, on either side."""
+    L = lib()
+    n = 2 ** 28 + 3
+    print(f"product {n}x{few}x16", flush=True)
+    first = torch.randint(-128, 128, (PERIOD, 16), generator=gen(4), device="cuda", dtype=torch.int8)
+    a = torch.empty((n, 16), dtype=torch.int8, device="cuda")
+    m = n // PERIOD * PERIOD
+    a[:m].unflatten(0, (-1, PERIOD)).copy_(first.expand(m // PERIOD, PERIOD, 16))
+    a[m:] = first[:n - m]
+    b = torch.randint(-128, 128, (few, 16), generator=gen(5), device="cuda", dtype=torch.int8)
+    one = torch.full((1,), 2.0 ** -4, device="cuda")
+    want = ((first.double() @ b.double().t().contiguous()) * 2.0 ** -8).half()     # one rounding
+    c = L.matmul(a, b.t(), scale_a=one, scale_b=one, out_dtype=torch.float16)
+    assert torch.equal(c[:PERIOD], want)
+    check_repeats(c, "rows of A")
+    c = L.matmul(b, a.t(), scale_a=one, scale_b=one, out_dtype=torch.float16).t()
+    assert torch.equal(c[:PERIOD], want)
+    check_repeats(c, "columns of B")
