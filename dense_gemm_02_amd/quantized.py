@@ -64,7 +64,8 @@ def takes_stream(fn):
         if stream is None:
             return fn(*args, **kw)
         import torch
-        device = one_device("the arguments", args[0] if args else next(iter(kw.values()), None))
+        # (Any tensor tells: keywords come in any order, None and numbers among them.)
+        device = one_device("the arguments", next((t for t in (*args, *kw.values()) if hasattr(t, "is_cuda")), None))
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
         if stream.device != device:

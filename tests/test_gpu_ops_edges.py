@@ -149,3 +149,37 @@ def test_product_of_more_strips_than_a_launch(few):
     c = L.matmul(b, a.t(), scale_a=one, scale_b=one, out_dtype=torch.float16).t()
     assert torch.equal(c[:PERIOD], want)
     check_repeats(c, "columns of B")
+
+
+def test_stream_with_keywords_in_any_order():
+    L = lib()
+    g = gen(6)
+    ids = torch.randint(0, 8, (50, 2), generator=g, device="cuda")
+    x = torch.randn((50, 64), generator=g, device="cuda")
+    w = torch.rand((50, 2), generator=g, device="cuda")
+    b = torch.randint(-128, 128, (8, 32, 64), generator=g, device="cuda", dtype=torch.int8)
+    sb = torch.rand((8, 32), generator=g, device="cuda")
+    offsets, slot, _, token = L.expert_sort(ids, 8, with_token=True)
+    q, s = L.quantize_i8(x)
+    y = L.expert_dispatch(x, slot)
+    calls = [
+        lambda kw: L.expert_sort(experts=8, with_token=True, ids=ids, **kw),
+        lambda kw: L.quantize_i8(out=None, scale=None, x=x, **kw),
+        lambda kw: L.expert_dispatch(rows=100, out=None, slot=slot, x=x, **kw),
+        lambda kw: L.expert_combine(weights=None, out=None, y=y, slot=slot, **kw),
+        lambda kw: L.expert_dispatch_grad(out=None, dy=y, slot=slot, **kw),
+        lambda kw: L.expert_combine_grad(dy=None, dweights=None, weights=w, dout=x, y=y, slot=slot, **kw),
+        lambda kw: L.matmul(out_dtype=torch.bfloat16, scale_a=s, scale_b=sb[0], b=b[0].t(), a=q, **kw),
+        lambda kw: L.matmul_grouped(out_dtype=torch.float16, out=None, row_index=token, scale_a=s, scale_b=sb, b=b, a=q,
+                                    offsets=offsets, **kw),
+        lambda kw: L.matmul_experts(out=None, weights=w, scale_b=sb, b=b, ids=ids, x=x, **kw),
+    ]
+    side = torch.cuda.Stream()
+    for i, call in enumerate(calls):
+        want = call({})
+        torch.cuda.synchronize()
+        for stream in (side, side.cuda_stream, 0):
+            got = call({"stream": stream})
+            torch.cuda.synchronize()
+            for a, c in zip(*((r if isinstance(r, tuple) else (r,)) for r in (got, want))):
+                assert torch.equal(a, c), i

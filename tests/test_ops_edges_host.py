@@ -48,3 +48,32 @@ def test_int8_strips_give_way_to_blocks(lib):  # noqa: F811
 def test_grouped_tiles_past_a_launch_are_refused(lib):  # noqa: F811
     n = 2 ** 17
     assert grouped(lib, G=n, rows=n, N=8192, ra=n, na=1, nb=1, gb=0, ldc=8192) == UNSUP
+
+
+class Elsewhere:
+    """Stands for a tensor, or a stream, of a device this host need not have."""
+    is_cuda = True
+
+    def __init__(self, index):
+        self.device = torch.device("cuda", index)
+
+
+class OtherStream:
+    device = torch.device("cuda", 1)
+
+
+def test_stream_finds_the_device_in_any_argument():
+    """A stream of another device than the tensors' is refused as such, which
+    takes their device: from any position, number or None before it."""
+    from dense_gemm_02_amd.quantized import takes_stream
+    ran = []
+    call = takes_stream(lambda *args, **kw: ran.append((args, kw)))
+    t = Elsewhere(0)
+    for args, kw in (((t,), {}), ((), {"ids": t}), ((), {"experts": 8, "ids": t}), ((), {"out": None, "x": t}),
+                     ((), {"out_dtype": torch.float16, "x": t}), ((8, t), {})):
+        with pytest.raises(ValueError, match="stream is on cuda:1"):
+            call(*args, stream=OtherStream(), **kw)
+    for args, kw in (((), {}), ((8,), {"out": None}), ((), {"x": torch.zeros(3)})):
+        with pytest.raises(TypeError, match="device tensors"):
+            call(*args, stream=OtherStream(), **kw)
+    assert not ran
