@@ -154,6 +154,11 @@ def matmul_experts(x, ids, weights, b, scale_b, out=None):
     ``matmul_grouped`` takes them.  Each token is quantised once; the products
     read its row through the sort, so no sorted copy of x is made.
     """
+    one_device("x, ids, weights, b, scale_b and out", x, ids, weights, b, scale_b, out)
+    if x.dim() != 2 or ids.dim() != 2 or x.shape[0] != ids.shape[0]:
+        raise ValueError(f"x {tuple(x.shape)} and ids {tuple(ids.shape)} must have one row for each token")
+    if b.dim() != 3 or x.shape[1] != b.shape[2]:
+        raise ValueError(f"x {tuple(x.shape)} and b {tuple(b.shape)} do not chain")
     q, scale = quantize_i8(x)
     offsets, slot, _, token = expert_sort(ids, b.shape[0], with_token=True)
     y = matmul_grouped(q, b, offsets, scale, scale_b, out_dtype=x.dtype, row_index=token)

@@ -183,3 +183,21 @@ def test_stream_with_keywords_in_any_order():
             torch.cuda.synchronize()
             for a, c in zip(*((r if isinstance(r, tuple) else (r,)) for r in (got, want))):
                 assert torch.equal(a, c), i
+
+
+def test_experts_layer_refuses_other_tokens():
+    """Fewer or more rows of x than of ids: neither zeros nor rows left out."""
+    L = lib()
+    b = torch.ones((3, 32, 64), dtype=torch.int8, device="cuda")
+    sb = torch.ones((3, 32), device="cuda")
+    x = torch.randn((6, 64), device="cuda")
+    for T in (0, 1, 5, 7, 9):
+        ids = torch.zeros((T, 2), dtype=torch.int64, device="cuda")
+        with pytest.raises(ValueError, match="one row for each token"):
+            L.matmul_experts(x, ids, torch.ones((T, 2), device="cuda"), b, sb)
+    ids, w = torch.zeros((6, 2), dtype=torch.int64, device="cuda"), torch.ones((6, 2), device="cuda")
+    with pytest.raises(ValueError, match="do not chain"):
+        L.matmul_experts(x[:, :48], ids, w, b, sb)
+    with pytest.raises(TypeError):
+        L.matmul_experts(x, ids.cpu(), w, b, sb)
+    assert L.matmul_experts(x, ids, w, b, sb).shape == (6, 32)

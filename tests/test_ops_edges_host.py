@@ -77,3 +77,21 @@ def test_stream_finds_the_device_in_any_argument():
         with pytest.raises(TypeError, match="device tensors"):
             call(*args, stream=OtherStream(), **kw)
     assert not ran
+
+
+class Shaped(Elsewhere):
+    def __init__(self, *shape):
+        super().__init__(0)
+        self.shape = shape
+
+    def dim(self):
+        return len(self.shape)
+
+
+@pytest.mark.parametrize("x,ids,b", [((5, 64), (7, 2), (3, 32, 64)), ((7, 64), (5, 2), (3, 32, 64)),
+                                     ((5, 64), (10,), (3, 32, 64)), ((64,), (1, 2), (3, 32, 64)),
+                                     ((5, 60), (5, 2), (3, 32, 64)), ((5, 64), (5, 2), (32, 64))])
+def test_experts_layer_refuses_what_does_not_match(x, ids, b):
+    import dense_gemm_02_amd as L
+    with pytest.raises(ValueError, match="one row for each token|do not chain"):
+        L.matmul_experts(Shaped(*x), Shaped(*ids), None, Shaped(*b), Shaped(3, 32))
