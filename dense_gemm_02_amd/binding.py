@@ -318,7 +318,8 @@ def matmul(a, b, out=None, scale_a=None, scale_b=None, stream=None, out_dtype=No
     if a.stride(1) != 1 and M * K > 1:
         raise ValueError("a must be row-major (stride(1) == 1)")
     lda = a.stride(0) if M > 1 else max(K, 1)
-    if b.stride(1) == 1 and (b.stride(0) != 1 or N == 1):
+    # (A vector as K x 1, strides (1, 1): a column contiguous along K.)
+    if b.stride(1) == 1 and (b.stride(0) != 1 or (N == 1 and K <= 1)):
         layout, ldb = "nn", (b.stride(0) if K > 1 else max(N, 1))
     elif b.stride(0) == 1:
         layout, ldb = "tn", (b.stride(1) if N > 1 else max(K, 1))

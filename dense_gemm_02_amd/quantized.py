@@ -167,7 +167,8 @@ def matmul_i8(a, b, scale_a, scale_b, out=None, out_dtype=None):
     M, K = a.shape
     N = b.shape[1]
     lda = pitch(a, "a", 16)
-    if b.stride(1) == 1 and (b.stride(0) != 1 or N == 1):
+    # (A vector as K x 1, strides (1, 1): a column contiguous along K.)
+    if b.stride(1) == 1 and (b.stride(0) != 1 or (N == 1 and K <= 1)):
         layout, ldb = 0, (b.stride(0) if K > 1 else -(-max(N, 1) // 16) * 16)
     elif b.stride(0) == 1 or K == 1:
         layout, ldb = 1, (b.stride(1) if N > 1 else -(-max(K, 1) // 16) * 16)

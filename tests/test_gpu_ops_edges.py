@@ -201,3 +201,36 @@ def test_experts_layer_refuses_other_tokens():
     with pytest.raises(TypeError):
         L.matmul_experts(x, ids.cpu(), w, b, sb)
     assert L.matmul_experts(x, ids, w, b, sb).shape == (6, 32)
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.float32, torch.float16, torch.bfloat16],
+                         ids=["i8", "f32", "f16", "bf16"])
+def test_product_with_a_vector_as_a_column(dtype):
+    """A vector v as v[:, None] (strides (1, 1)), as a transposed row and as
+    a column of a matrix.  Whole numbers: every sum is exact.  K of 1 has one
+    row of B, whose pitch the stride does not tell: int8 rounds it up to 16
+    bytes, the other types refuse it as misaligned."""
+    L = lib()
+    g = gen(8)
+    for M, K in ((1, 64), (40, 64), (300, 1008), (20, 1)):
+        a = torch.randint(-2, 3, (M, -(-K // 16) * 16), generator=g, device="cuda")[:, :K]
+        v = torch.randint(-2, 3, (K,), generator=g, device="cuda")
+        want = (a.double() @ v.double()[:, None])
+        a = torch.empty((M, -(-K // 16) * 16), device="cuda", dtype=dtype)[:, :K].copy_(a)
+        wide = torch.zeros((max(K, 16), 16), device="cuda", dtype=dtype)
+        wide[:K, 0] = v.to(dtype)
+        flat = torch.zeros(max(K, 16), device="cuda", dtype=dtype)[:K].copy_(v)
+        kw = {} if dtype != torch.int8 else dict(scale_a=torch.ones(1, device="cuda"), scale_b=torch.ones(1, device="cuda"))
+        forms = [wide[:K, :1]] if K == 1 else [wide[:K, :1], flat[:, None], flat[None].t()]
+        for b in forms:
+            print(f"vector {dtype} {M}x1x{K} strides {b.stride()}", flush=True)
+            if K == 1 and dtype != torch.int8:
+                with pytest.raises(L.DgemmError) as e:
+                    L.matmul(a, b)
+                assert e.value.status == 5
+                continue
+            c = L.matmul(a, b, **kw)
+            assert c.shape == (M, 1) and torch.equal(c.double(), want.to(c.dtype).double())
+        if K > 1:
+            out = torch.empty((M, 1), device="cuda", dtype=c.dtype)
+            assert L.matmul(a, flat[:, None], out=out, **kw) is out and torch.equal(out, c)
