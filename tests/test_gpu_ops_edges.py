@@ -234,3 +234,101 @@ def test_product_with_a_vector_as_a_column(dtype):
         if K > 1:
             out = torch.empty((M, 1), device="cuda", dtype=c.dtype)
             assert L.matmul(a, flat[:, None], out=out, **kw) is out and torch.equal(out, c)
+
+
+# ---- matrices past the caches -------------------------------------------------------
+# (From 96 MiB of rows on, quantize_i8 and the row operators take kernels of
+# their own, which read and write past the caches.)
+
+TYPES = [torch.float32, torch.float16, torch.bfloat16]
+IDS = ["f32", "f16", "bf16"]
+PAST = 96 << 20
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("packs", [1, 40, 64, 65, 128, 129, 250, 256, 257, 512, 513, 1000, 1025, 2048, 2049])
+def test_quantize_past_the_caches(packs, dtype):
+    """Every width of the register-held kernels, odd rows off every alignment."""
+    from test_gpu_quantized import check_quantize
+    per = 16 // dtype.itemsize
+    for K, off, pad in ((packs * per, 0, 0), (packs * per - 1, 1, 2)):
+        rows = PAST // (K * dtype.itemsize) + 3
+        print(f"quantize {rows}x{K} {dtype}", flush=True)
+        base = torch.randn((rows, K + off + pad), generator=gen(packs), device="cuda")
+        x = base.to(dtype)[:, off:off + K]
+        x[1::7] *= 2.0 ** -9
+        x[5] = 0
+        x[rows - 1, K - 1] = float("nan")
+        out = torch.full((rows, K + 3), 99, dtype=torch.int8, device="cuda")
+        check_quantize(x, out=out[:, 1:1 + K])
+        assert (out[:, 0] == 99).all() and (out[:, 1 + K:] == 99).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("k,H,off,pad", [(1, 512, 0, 0), (4, 501, 1, 2), (9, 130, 3, 0), (2, 4096, 0, 0), (3, 1031, 1, 2),
+                                         (8, 2056, 8, 8), (11, 700, 5, 1)])
+def test_rows_past_the_caches(k, H, off, pad, dtype):
+    """Short rows (one wave a token) and long ones, more choices than a batch,
+    odd pitches and offsets, dropped pairs; what lies between the rows stays."""
+    from test_gpu_experts import check_combine, check_grad, rows
+    L = lib()
+    H = H // 2 if dtype == torch.float32 and H <= 512 else H
+    T = PAST // (k * H * dtype.itemsize) + 3
+    print(f"rows {T}x{k} H={H} {dtype}", flush=True)
+    g = gen(H + k)
+    slot = torch.randperm(T * k, generator=g, device="cuda").int().reshape(T, k)
+    slot[torch.rand((T, k), generator=g, device="cuda") < 0.05] = -1
+    slot[0] = -1
+    w = torch.rand((T, k), generator=g, device="cuda")
+    ok = slot >= 0
+    n = slot[ok].long()
+    named = torch.zeros(T * k, dtype=torch.bool, device="cuda")
+    named[n] = True
+    x = rows(g, T, H, dtype, pad, off)
+    wide = torch.full((T * k, H + off + pad), 7.0, device="cuda").to(dtype)
+    L.expert_dispatch(x, slot, out=wide[:, off:off + H])
+    t_of = torch.arange(T, device="cuda")[:, None].expand(T, k)[ok]
+    assert torch.equal(wide[n, off:off + H], x[t_of])
+    assert (wide[~named] == 7).all() and (wide[:, :off] == 7).all() and (wide[:, off + H:] == 7).all()
+    y = rows(g, T * k, H, dtype, pad, off)
+    back = torch.full((T, H + off + pad), 7.0, device="cuda").to(dtype)
+    check_combine(y, slot, w, out=back[:, off:off + H])
+    assert (back[:, :off] == 7).all() and (back[:, off + H:] == 7).all()
+    check_combine(y, slot, None)
+    wide.fill_(7.0)
+    check_grad(x, y, slot, w, dy=wide[:, off:off + H])
+    assert (wide[:, :off] == 7).all() and (wide[:, off + H:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.int64, torch.int32], ids=["i64", "i32"])
+@pytest.mark.parametrize("T,k,E", [(524289, 1, 64), (131085, 8, 128), (262151, 2, 1024), (1500007, 3, 7), (2097153, 1, 1)])
+def test_sort_of_more_pairs_than_the_smallest_chunks(T, k, E, dtype):
+    """More than 256 chunks of 2048 pairs: the chunks grow."""
+    from test_gpu_experts import check_sort
+    print(f"sort {T}x{k} into {E} {dtype}", flush=True)
+    g = gen(T + E)
+    ids = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=dtype)
+    check_sort(ids, E)
+    ids[torch.rand((T, k), generator=g, device="cuda") < 0.1] = -1
+    ids[torch.rand((T, k), generator=g, device="cuda") < 0.05] = E
+    check_sort(ids, E)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("tile,M,N", [("16x16", 37, 213), ("32x64", 33, 4731), ("64x32", 19, 11295), ("128x16", 1, 26185)])
+def test_row_major_strips_store_at_any_alignment(tile, M, N, dtype):
+    """The row-major-B strips' results at every offset of a 16-byte grid."""
+    import ctypes
+    from test_gpu_quantized import exact, near, operands
+    L = lib()
+    buf = ctypes.create_string_buffer(256)
+    a, b, sa, sb = operands("nn", M, N, 272, 9)
+    assert L.load_library().dgemm_kernel_config(6 + TYPES.index(dtype), 0, M, N, 272, buf, 256) == 0
+    assert buf.value.decode().startswith("i8_nn_skinny tile=" + tile), buf.value
+    want = exact(a, b, sa, sb)
+    for off in range(16 // dtype.itemsize + 1):
+        for extra in (9, 10, 16):
+            print(f"nn skinny {tile} {dtype} offset {off} pitch {N + extra}", flush=True)
+            wide = torch.full((M, N + extra), 7.0, device="cuda").to(dtype)
+            near(L.matmul(a, b, scale_a=sa, scale_b=sb, out=wide[:, off:off + N]), want)
+            assert (wide[:, :off] == 7).all() and (wide[:, off + N:] == 7).all()
