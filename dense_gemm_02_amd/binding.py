@@ -84,6 +84,8 @@ def load_library():
     L.dgemm_lds_bytes.restype = i64
     L.dgemm_kernel_config.argtypes = [ci, ci, i64, i64, i64, ctypes.c_char_p, i64]
     L.dgemm_kernel_config.restype = ci
+    L.dgemm_grouped_config.argtypes = [ci, ci, i64, i64, i64, i64, ctypes.c_char_p, i64]
+    L.dgemm_grouped_config.restype = ci
     L.dgemm_trace_clock.argtypes = [vp, i64]
     L.dgemm_trace_clock.restype = ci
     _lib = L

@@ -1,5 +1,6 @@
 // gemm_i8_grouped: argument checks, kernel choice and launch.
 #include <math.h>
+#include <stdio.h>
 #include <stdlib.h>
 #include <string.h>
 
@@ -143,6 +144,24 @@ int choose_kind(int64_t groups, int64_t rows, int64_t N, int64_t K) {
   return best;
 }
 
+struct GroupedPlan {
+  Launch L;
+  int64_t tiles_p, tiles_q;
+};
+
+// The kernel and its workgroups: for the most row tiles that `rows` rows in
+// `groups` groups can have, every group with rows may end in a part-filled
+// one.  False if no launch holds them.
+bool plan_grouped(int64_t groups, int64_t rows, int64_t N, int64_t K, int c_type, bool gather, GroupedPlan* pl) {
+  const int kind = choose_kind(groups, rows, N, K);
+  const bool kt = K % 128 != 0;
+  pl->L = gather ? launch_for<true>(c_type, kind, kt) : launch_for<false>(c_type, kind, kt);
+  pl->tiles_p = (N + pl->L.bp - 1) / pl->L.bp;
+  const int64_t some = groups < rows ? groups : rows;
+  pl->tiles_q = (rows + some * (pl->L.bq - 1)) / pl->L.bq;
+  return launchable(pl->tiles_p * pl->tiles_q, pl->L.threads);
+}
+
 constexpr int64_t kMaxCount = 0x7fffffff;
 
 bool aligned(const void* p, int64_t n) { return ((uintptr_t)p) % (uintptr_t)n == 0; }
@@ -150,10 +169,12 @@ bool aligned(const void* p, int64_t n) { return ((uintptr_t)p) % (uintptr_t)n ==
 }  // namespace
 }  // namespace dg
 
-extern "C" int gemm_i8_grouped(int64_t groups, int64_t rows, int64_t N, int64_t K, const int8_t* A, int64_t rows_a,
-                               int64_t lda, const int32_t* row_index, const int8_t* B, int64_t ldb, int64_t group_b,
-                               void* C, int64_t ldc, int c_type, const float* scale_a, int64_t n_scale_a,
-                               const float* scale_b, int64_t n_scale_b, const int32_t* offsets, void* stream) {
+extern "C" {
+
+int gemm_i8_grouped(int64_t groups, int64_t rows, int64_t N, int64_t K, const int8_t* A, int64_t rows_a, int64_t lda,
+                    const int32_t* row_index, const int8_t* B, int64_t ldb, int64_t group_b, void* C, int64_t ldc,
+                    int c_type, const float* scale_a, int64_t n_scale_a, const float* scale_b, int64_t n_scale_b,
+                    const int32_t* offsets, void* stream) {
   using namespace dg;
   if (c_type < DGEMM_F32 || c_type > DGEMM_BF16) return DGEMM_ERR_INVALID_TYPE;
   if (groups < 0 || rows < 0 || N < 0 || K < 0 || rows_a < 0 || group_b < 0) return DGEMM_ERR_INVALID_DIM;
@@ -183,9 +204,8 @@ extern "C" int gemm_i8_grouped(int64_t groups, int64_t rows, int64_t N, int64_t 
   // An index over no rows: every row counts as zeros, as with K == 0.
   if (rows_a == 0) K = 0;
 
-  const int kind = choose_kind(groups, rows, N, K);
-  const bool kt = K % 128 != 0;
-  const Launch L = row_index != nullptr ? launch_for<true>(c_type, kind, kt) : launch_for<false>(c_type, kind, kt);
+  GroupedPlan pl;
+  if (!plan_grouped(groups, rows, N, K, c_type, row_index != nullptr, &pl)) return DGEMM_ERR_UNSUPPORTED;
   GroupedArgs a{};
   GemmArgs& g = a.g;
   g.P = (const char*)B; g.ldp = ldb; g.Pn = N;
@@ -196,12 +216,30 @@ extern "C" int gemm_i8_grouped(int64_t groups, int64_t rows, int64_t N, int64_t 
   g.sq = scale_a; g.sq_row = n_scale_a > 1 ? 1 : 0;
   a.offsets = offsets; a.groups = groups; a.rows = rows; a.pstride = group_b;
   a.gt.index = row_index; a.gt.rows = rows_a;
-  // Workgroups for the most row tiles that `rows` rows in `groups` groups
-  // can have: every group with rows may end in a part-filled one.
-  g.tiles_p = (N + L.bp - 1) / L.bp;
-  const int64_t some = groups < rows ? groups : rows;
-  g.tiles_q = (rows + some * (L.bq - 1)) / L.bq;
-  const int64_t grid = g.tiles_p * g.tiles_q;
-  if (!launchable(grid, L.threads)) return DGEMM_ERR_UNSUPPORTED;
-  return launch_kernel(L.fn, grid, L.threads, &a, stream);
+  g.tiles_p = pl.tiles_p;
+  g.tiles_q = pl.tiles_q;
+  return launch_kernel(pl.L.fn, pl.tiles_p * pl.tiles_q, pl.L.threads, &a, stream);
 }
+
+int dgemm_grouped_config(int c_type, int gather, int64_t groups, int64_t rows, int64_t N, int64_t K, char* buf,
+                         int64_t len) {
+  using namespace dg;
+  if (c_type < DGEMM_F32 || c_type > DGEMM_BF16) return DGEMM_ERR_INVALID_TYPE;
+  if (groups < 0 || rows < 0 || N < 0 || K < 0) return DGEMM_ERR_INVALID_DIM;
+  if (groups > kMaxCount || N > kMaxCount || groups * N > kMaxCount) return DGEMM_ERR_UNSUPPORTED;
+  if (rows > kMaxDescBytes / 4 || N > kMaxDescBytes / 4 || K > kMaxI8K) return DGEMM_ERR_UNSUPPORTED;
+  GroupedPlan pl{};
+  const bool none = rows == 0 || N == 0 || groups == 0;
+  if (!none && !plan_grouped(groups, rows, N, K, c_type, gather != 0, &pl)) return DGEMM_ERR_UNSUPPORTED;
+  if (buf != nullptr && len > 0) {
+    if (none)
+      snprintf(buf, (size_t)len, "none (empty output)");
+    else
+      snprintf(buf, (size_t)len, "%s tile=%dx%d threads=%d lds=%d grid=%lld tiles=%lldx%lld", pl.L.name, pl.L.bp,
+               pl.L.bq, pl.L.threads, pl.L.lds, (long long)(pl.tiles_p * pl.tiles_q), (long long)pl.tiles_p,
+               (long long)pl.tiles_q);
+  }
+  return DGEMM_OK;
+}
+
+}  // extern "C"

@@ -299,6 +299,9 @@ const char* dgemm_hip_error_string(int code);
  * 2 bf16, 3 fp8, 4 fp8 with scale factors, 5 MXFP8, 6 / 7 / 8 int8 with
  * FP32 / FP16 / BF16 results.  Returns 0, or a
  * dgemm_status for invalid arguments.
+ *
+ * dgemm_grouped_config: the same for gemm_i8_grouped with results of c_type
+ * (a dgemm_type), with (gather != 0) or without a row_index.
  */
 /*
  * dgemm_trace_clock (diagnostics, used to report the engine clock the GEMM
@@ -321,6 +324,8 @@ int dgemm_tile_map(int64_t tiles_p, int64_t tiles_q, int64_t group, int64_t pid,
                    int64_t* tile_p, int64_t* tile_q);
 int64_t dgemm_lds_bytes(int bm, int bn, int bk, int elem, int pad_bytes, int buffers);
 int dgemm_kernel_config(int dtype, int layout, int64_t M, int64_t N, int64_t K, char* buf, int64_t len);
+int dgemm_grouped_config(int c_type, int gather, int64_t groups, int64_t rows, int64_t N, int64_t K, char* buf,
+                         int64_t len);
 
 #ifdef __cplusplus
 }

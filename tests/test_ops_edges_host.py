@@ -95,3 +95,80 @@ def test_experts_layer_refuses_what_does_not_match(x, ids, b):
     import dense_gemm_02_amd as L
     with pytest.raises(ValueError, match="one row for each token|do not chain"):
         L.matmul_experts(Shaped(*x), Shaped(*ids), None, Shaped(*b), Shaped(3, 32))
+
+
+# ---- the kernels that the GPU tests force by name -----------------------------------
+
+@pytest.mark.parametrize("tag,code", [("i8f", 6), ("i8h", 7), ("i8b", 8)])
+def test_forced_dense_kernels_are_the_named_ones(lib, monkeypatch, tag, code):  # noqa: F811
+    """A name that no kernel bears would leave the choice as it was."""
+    from test_gpu_quantized import TILES_NN, TILES_TN
+    for layout, tiles in ((1, TILES_TN), (0, TILES_NN)):
+        for tile in tiles:
+            want = f"{tag}_{'tn' if layout else 'nn'}_{tile}"
+            monkeypatch.setenv("DGEMM_CONFIG", want)
+            for M, N in ((300, 333), (303, 290)):
+                for K in (1, 16, 100, 128, 129, 200, 256, 257, 272, 384, 399, 512, 600, 639):
+                    st, _, name = config(lib, code, layout, M, N, K)
+                    assert st == OK and name == want, (name, want, K)
+
+
+def grouped_config(lib, c_type, gather, groups, rows, N, K):  # noqa: F811
+    buf = ctypes.create_string_buffer(256)
+    st = lib.dgemm_grouped_config(c_type, gather, groups, rows, N, K, buf, 256)
+    words = buf.value.decode().split()
+    return st, dict(x.split("=") for x in words[1:] if "=" in x), words[0] if words else ""
+
+
+GROUPED = ["256x256_pp", "128x128_w4", "128x128_w4_s4", "128x64_w4_s4", "skinny16", "skinny32", "skinny64"]
+
+
+@pytest.mark.parametrize("kernel", GROUPED)
+def test_forced_grouped_kernels_are_the_named_ones(lib, monkeypatch, kernel):  # noqa: F811
+    import test_gpu_quantized as T
+    for test in (T.test_grouped_every_kernel, T.test_grouped_stores_at_any_alignment):
+        marks = [m for m in test.pytestmark if m.name == "parametrize" and m.args[0] == "kernel"]
+        assert marks and list(marks[0].args[1]) == GROUPED
+    monkeypatch.setenv("DGEMM_CONFIG", "i8_grouped_" + kernel)
+    for c_type in (0, 1, 2):
+        for gather in (0, 1):
+            for groups, rows, N in ((7, 87, 70), (6, 550, 300), (3, 306, 513), (70, 215, 40), (4, 338, 141)):
+                for K in (1, 100, 128, 200, 256, 399, 1040):
+                    st, _, name = grouped_config(lib, c_type, gather, groups, rows, N, K)
+                    assert st == OK and name == "i8_grouped_" + kernel, (name, K)
+
+
+def test_every_grouped_kernel_is_chosen_somewhere(lib):  # noqa: F811
+    seen = {grouped_config(lib, 2, 1, g, r, N, K)[2]
+            for g in (1, 2, 8, 64, 256) for r in (8, 64, 256, 512, 1024, 2048, 8192, 32768)
+            for N in (256, 1024, 2048, 4096, 14336) for K in (64, 256, 1024, 4096, 14336)}
+    assert seen == {"i8_grouped_" + k for k in GROUPED}
+
+
+def test_grouped_config_refusals(lib):  # noqa: F811
+    assert grouped_config(lib, 3, 0, 4, 10, 20, 30)[0] == 8 and grouped_config(lib, -1, 0, 4, 10, 20, 30)[0] == 8
+    for bad in ((-1, 10, 20, 30), (4, -1, 20, 30), (4, 10, -1, 30), (4, 10, 20, -1)):
+        assert grouped_config(lib, 0, 0, *bad)[0] == 1
+    for bad in ((2 ** 31, 1, 1, 1), (1, 1, 2 ** 31, 1), (2 ** 16, 1, 2 ** 16, 1), (1, 2 ** 29, 1, 1), (1, 1, 2 ** 29, 1),
+                (1, 1, 1, 131072), (2 ** 17, 2 ** 17, 8192, 32)):
+        assert grouped_config(lib, 0, 0, *bad)[0] == UNSUP
+    for none in ((0, 10, 20, 30), (4, 0, 20, 30), (4, 10, 0, 30)):
+        st, _, name = grouped_config(lib, 0, 1, *none)
+        assert st == OK and name == "none"
+    assert lib.dgemm_grouped_config(0, 0, 4, 10, 20, 30, None, 0) == OK
+    short = ctypes.create_string_buffer(b"x" * 16)
+    assert lib.dgemm_grouped_config(0, 0, 4, 10, 20, 30, short, 8) == OK and short.raw[7:9] == b"\0x"
+
+
+def test_grouped_launches_stay_below_the_limit(lib):  # noqa: F811
+    """What the header promises of the sizes that fit, and no grid past them."""
+    for g in (1, 3, 64, 1000, 2 ** 17, 2 ** 20):
+        for rows in (1, 100, 2 ** 14, 2 ** 20, 2 ** 26 + 1, 2 ** 29 - 16):
+            for N in (1, 32, 33, 1000, 2047):
+                if g * N > 2 ** 31 - 1:
+                    continue
+                for K in (1, 1000, 100000):
+                    st, c, _ = grouped_config(lib, 2, 0, g, rows, N, K)
+                    if -(-N // 32) * 32 * (rows + 15 * g) < 2 ** 32:
+                        assert st == OK
+                    assert st == UNSUP or int(c["grid"]) * int(c["threads"]) < 2 ** 32
