@@ -164,6 +164,10 @@ bool plan_grouped(int64_t groups, int64_t rows, int64_t N, int64_t K, int c_type
 
 constexpr int64_t kMaxCount = 0x7fffffff;
 
+// Every wave looks through the groups 64 at a time (gemm_grouped.hpp, whose
+// counter of groups has 32 bits): 2^14 steps at this many.
+constexpr int64_t kMaxGroups = int64_t(1) << 20;
+
 bool aligned(const void* p, int64_t n) { return ((uintptr_t)p) % (uintptr_t)n == 0; }
 
 }  // namespace
@@ -178,7 +182,7 @@ int gemm_i8_grouped(int64_t groups, int64_t rows, int64_t N, int64_t K, const in
   using namespace dg;
   if (c_type < DGEMM_F32 || c_type > DGEMM_BF16) return DGEMM_ERR_INVALID_TYPE;
   if (groups < 0 || rows < 0 || N < 0 || K < 0 || rows_a < 0 || group_b < 0) return DGEMM_ERR_INVALID_DIM;
-  if (groups > kMaxCount || N > kMaxCount || groups * N > kMaxCount) return DGEMM_ERR_UNSUPPORTED;
+  if (groups > kMaxGroups || N > kMaxCount || groups * N > kMaxCount) return DGEMM_ERR_UNSUPPORTED;
   if ((n_scale_a != 1 && n_scale_a != rows_a) || (n_scale_b != 1 && n_scale_b != groups * N))
     return DGEMM_ERR_INVALID_DIM;
   if (row_index == nullptr && rows_a < rows) return DGEMM_ERR_INVALID_DIM;
@@ -226,7 +230,7 @@ int dgemm_grouped_config(int c_type, int gather, int64_t groups, int64_t rows, i
   using namespace dg;
   if (c_type < DGEMM_F32 || c_type > DGEMM_BF16) return DGEMM_ERR_INVALID_TYPE;
   if (groups < 0 || rows < 0 || N < 0 || K < 0) return DGEMM_ERR_INVALID_DIM;
-  if (groups > kMaxCount || N > kMaxCount || groups * N > kMaxCount) return DGEMM_ERR_UNSUPPORTED;
+  if (groups > kMaxGroups || N > kMaxCount || groups * N > kMaxCount) return DGEMM_ERR_UNSUPPORTED;
   if (rows > kMaxDescBytes / 4 || N > kMaxDescBytes / 4 || K > kMaxI8K) return DGEMM_ERR_UNSUPPORTED;
   GroupedPlan pl{};
   const bool none = rows == 0 || N == 0 || groups == 0;

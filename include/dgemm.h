@@ -184,7 +184,7 @@ int gemm_i8_scaled(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda
  * A readable over rows_a*lda and B over (groups - 1)*group_b + N*ldb bytes;
  * offsets, row_index and the factors 4-byte, C element-aligned.
  * Checks, in this order: c_type; negative extents or group_b ->
- * DGEMM_ERR_INVALID_DIM; groups, N or groups*N above 2^31 - 1 ->
+ * DGEMM_ERR_INVALID_DIM; groups above 2^20, N or groups*N above 2^31 - 1 ->
  * DGEMM_ERR_UNSUPPORTED; factor counts, rows_a against rows ->
  * DGEMM_ERR_INVALID_DIM; rows == 0, N == 0 or groups == 0 -> DGEMM_OK with no
  * work; NULL pointers (A and B may be NULL if K == 0, A and scale_a if

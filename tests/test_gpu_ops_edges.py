@@ -332,3 +332,22 @@ def test_row_major_strips_store_at_any_alignment(tile, M, N, dtype):
             wide = torch.full((M, N + extra), 7.0, device="cuda").to(dtype)
             near(L.matmul(a, b, scale_a=sa, scale_b=sb, out=wide[:, off:off + N]), want)
             assert (wide[:, :off] == 7).all() and (wide[:, off + N:] == 7).all()
+
+
+@pytest.mark.parametrize("gather", [False, True], ids=["sorted", "gather"])
+def test_grouped_as_many_groups_as_it_takes(gather):
+    """2^20 groups, nearly all of them empty, sharing one weight."""
+    from test_gpu_quantized import factors, grouped_exact, ints, near
+    L = lib()
+    G, rows, N, K = 2 ** 20, 300, 40, 48
+    g = gen(12)
+    at = torch.sort(torch.randint(0, G, (rows,), generator=g, device="cuda"))[0]
+    at[:40], at[-40:] = 0, G - 1
+    off = torch.zeros(G + 1, dtype=torch.int32, device="cuda")
+    off[1:] = torch.bincount(at, minlength=G).cumsum(0)
+    b = ints(g, (1, N, K))
+    a, sa, one = ints(g, (rows, K)), factors(g, rows), torch.full((1,), 0.5, device="cuda")
+    idx = torch.randint(0, rows, (rows,), generator=g, device="cuda", dtype=torch.int32) if gather else None
+    got = L.matmul_grouped(a, b.expand(G, N, K), off, sa, one, row_index=idx)
+    whole = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    near(got, grouped_exact(a, b, whole, sa, one, idx, rows))

@@ -172,3 +172,13 @@ def test_grouped_launches_stay_below_the_limit(lib):  # noqa: F811
                     if -(-N // 32) * 32 * (rows + 15 * g) < 2 ** 32:
                         assert st == OK
                     assert st == UNSUP or int(c["grid"]) * int(c["threads"]) < 2 ** 32
+
+
+def test_grouped_groups_past_the_search_are_refused(lib):  # noqa: F811
+    """The search over the groups counts them in 32 bits, 64 at a time: with
+    2^31 - 1 of them it would never end."""
+    for n in (2 ** 20 + 1, 2 ** 31 - 64, 2 ** 31 - 63, 2 ** 31 - 1):
+        assert grouped(lib, G=n, N=1, ldc=1, nb=1, gb=0, rows=1, ra=1, na=1) == UNSUP
+        assert grouped(lib, G=n, N=1, ldc=1, nb=1, gb=0, rows=0) == UNSUP      # before the calls without work
+        assert grouped_config(lib, 0, 0, n, 1, 1, 32)[0] == UNSUP
+    assert grouped_config(lib, 0, 0, 2 ** 20, 1, 1, 32)[0] == OK
