@@ -10,7 +10,6 @@ namespace dg {
 
 inline int type_bytes(int type) { return type == DGEMM_F32 ? 4 : 2; }
 inline bool valid_type(int type) { return type >= DGEMM_F32 && type <= DGEMM_BF16; }
-inline bool aligned_to(const void* p, int64_t n) { return ((uintptr_t)p) % (uintptr_t)n == 0; }
 
 // Row matrices of this many bytes and more are read once and written past the
 // caches (nontemporal).  Measured on tokens dispatched to eight rows of 8 KiB
@@ -48,7 +47,6 @@ struct Pack {
 // Sixteen bytes at the alignment of T.  (gfx950 serves global accesses of any
 // alignment; 16-byte ones of aligned and unaligned rows are the same
 // instruction.)
-typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
 template <class T>
 struct Unaligned {

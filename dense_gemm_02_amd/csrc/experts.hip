@@ -7,7 +7,6 @@ namespace dg {
 namespace {
 
 constexpr int kMaxExperts = 1024;
-constexpr int64_t kMaxCount = 0x7fffffff;
 
 // ---- sort -------------------------------------------------------------------------
 //

@@ -212,7 +212,6 @@ __device__ __forceinline__ u32x4 mask_tail(u32x4 v, int valid_bytes) {
 // an aligned one, against 86 in blocks on the 16-byte grid.
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x2 u32x2_at2 __attribute__((aligned(2)));
-typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
 template <class Op>
 __device__ __forceinline__ void store4(const GemmArgs& a, int64_t q, int64_t p, float v0, float v1, float v2,
                                        float v3) {

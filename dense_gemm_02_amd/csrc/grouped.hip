@@ -112,6 +112,14 @@ Launch launch_for(int c_type, int kind, bool kt) {
 //   12054 rows, 79 groups, N 1021, K 445    41 /  37 /  57 /  64 /  184 /  133
 //   4096 rows, 8 groups, N 4096, K 128      16 /  20 /  34 /  43 /  140 /  109
 //   512 rows, 64 groups, N 2048, K 256      22 /  14 /  24 /  21 /   23 /   32
+// The skinny kernel of 64 is estimated fastest where one tile a CU covers all
+// rows; there it runs within a tenth of that of 32 (256 x 256 / 128 x 128 / four
+// stages / 128 x 64 / skinny of 16 / of 32 / of 64):
+//   256 rows, 2 groups, N 2048, K 4096       42 / 35 / 31 / 21 / 19 / 17 / 18
+//   512 rows, 4 groups, N 1024, K 4096       42 / 36 / 31 / 21 / 21 / 17 / 18
+//   128 rows, 2 groups, N 4096, K 8192       74 / 63 / 52 / 36 / 35 / 32 / 35
+//   1024 rows, 16 groups, N 512, K 8192      76 / 66 / 53 / 36 / 36 / 32 / 34
+//   512 rows, 5 groups, N 1024, K 1024       17 / 13 / 15 / 12 / 12 / 12 / 12
 int choose_kind(int64_t groups, int64_t rows, int64_t N, int64_t K) {
   const double cus = 256.0;
   const double some = (double)(groups < rows ? groups : rows);
@@ -162,13 +170,9 @@ bool plan_grouped(int64_t groups, int64_t rows, int64_t N, int64_t K, int c_type
   return launchable(pl->tiles_p * pl->tiles_q, pl->L.threads);
 }
 
-constexpr int64_t kMaxCount = 0x7fffffff;
-
 // Every wave looks through the groups 64 at a time (gemm_grouped.hpp, whose
 // counter of groups has 32 bits): 2^14 steps at this many.
 constexpr int64_t kMaxGroups = int64_t(1) << 20;
-
-bool aligned(const void* p, int64_t n) { return ((uintptr_t)p) % (uintptr_t)n == 0; }
 
 }  // namespace
 }  // namespace dg
@@ -194,10 +198,10 @@ int gemm_i8_grouped(int64_t groups, int64_t rows, int64_t N, int64_t K, const in
   const int64_t min_ld = K > 0 ? K : 1;
   if (lda < min_ld || ldb < min_ld || ldc < N) return DGEMM_ERR_INVALID_LD;
   const int oe = c_type == DGEMM_F32 ? 4 : 2;
-  if (K > 0 && (!aligned(A, 16) || !aligned(B, 16) || lda % 16 != 0 || ldb % 16 != 0 || group_b % 16 != 0))
+  if (K > 0 && (!aligned_to(A, 16) || !aligned_to(B, 16) || lda % 16 != 0 || ldb % 16 != 0 || group_b % 16 != 0))
     return DGEMM_ERR_MISALIGNED;
-  if (!aligned(C, oe) || !aligned(scale_a, 4) || !aligned(scale_b, 4) || !aligned(offsets, 4) ||
-      !aligned(row_index, 4))
+  if (!aligned_to(C, oe) || !aligned_to(scale_a, 4) || !aligned_to(scale_b, 4) || !aligned_to(offsets, 4) ||
+      !aligned_to(row_index, 4))
     return DGEMM_ERR_MISALIGNED;
   if (K > kMaxI8K || lda > kMaxDescBytes / 256 || ldb > kMaxDescBytes / 256) return DGEMM_ERR_UNSUPPORTED;
   // The factors of a group and of the rows, and with an index all rows of A

@@ -62,6 +62,11 @@ constexpr int64_t kMaxDescBytes = (int64_t(1) << 31) - 64;
 // The sum of K products of two int8 values fits 32 bits up to this K.
 constexpr int64_t kMaxI8K = 131071;
 
+// Rows, tokens, pairs and groups are counted in 32 bits on the device.
+constexpr int64_t kMaxCount = 0x7fffffff;
+
+inline bool aligned_to(const void* p, int64_t n) { return ((uintptr_t)p) % (uintptr_t)n == 0; }
+
 // HIP takes fewer than 2^32 work-items a launch.
 inline bool launchable(int64_t grid, int threads) { return grid <= 0xffffffffll / threads; }
 
