@@ -148,11 +148,15 @@ def expert_combine_grad(dout, y, slot, weights=None, dy=None, dweights=None):
 def matmul_experts(x, ids, weights, b, scale_b, out=None):
     """One linear layer of int8 experts: ``out[t] = sum_j weights[t, j] *
     (b[e] @ x[t])``, e = ids[t, j], with x quantised to int8 row by row.
+    Each product is rounded to x's type before its weight is applied (as a
+    sequence of layers would; one past float16's range is an infinity), the
+    weighted sum once more.
 
     x: [T, K], float32, float16 or bfloat16 (and so the result, [T, N]); ids,
     weights: [T, k]; b: int8, experts x N x K with scale_b experts x N, as
     ``matmul_grouped`` takes them.  Each token is quantised once; the products
-    read its row through the sort, so no sorted copy of x is made.
+    read its row through the sort, so no sorted copy of x is made.  T times K
+    (rounded up to 16) has to stay below 2^31.
     """
     one_device("x, ids, weights, b, scale_b and out", x, ids, weights, b, scale_b, out)
     if x.dim() != 2 or ids.dim() != 2 or x.shape[0] != ids.shape[0]:
