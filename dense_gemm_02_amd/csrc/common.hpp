@@ -186,4 +186,9 @@ __device__ __forceinline__ uint32_t gather_row(const Gather& gt, int64_t q, int6
   return (uint32_t)r < (uint32_t)gt.rows ? (uint32_t)(r * ld + chunk) : kOobOffset;
 }
 
+// Whether row q is none of the product's, or stands for no row of Q.
+__device__ __forceinline__ bool no_row(const Gather& gt, int64_t q, int64_t qn) {
+  return gather_row(gt, q, qn, 0, 0) != 0;
+}
+
 }  // namespace dg

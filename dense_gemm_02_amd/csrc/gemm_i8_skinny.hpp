@@ -96,6 +96,8 @@ __device__ __forceinline__ void gemm_i8_skinny_body(const GemmArgs& a, const Gat
     if constexpr (GA) ffo = lane < Cfg::FR ? gather_row(gt, lane, fn, fr * 4, 0) : kOobOffset;
     else if (lane < frows) ffo = (uint32_t)((lane >> fs) * fr * 4);
   }
+  // Few rows with a source, a bit each: the others are zeros (see staged_epilogue).
+  [[maybe_unused]] const uint64_t sources = BLK && GA ? __ballot(ffo != kOobOffset) : 0;
 
   // This wave's stages: every NW-th, from a place that differs between
   // workgroups, so that they do not all read the same part of the rows at once.
@@ -245,6 +247,8 @@ __device__ __forceinline__ void gemm_i8_skinny_body(const GemmArgs& a, const Gat
       EpiScale<1, 16, GA> sc;
       sc.init(a, lane, q0, gt);
       sc.apply(EpiScale<1, 16, GA>::p4(a, p), 0, v0, v1, v2, v3);
+    } else if constexpr (GA) {
+      if (!(sources >> (q0 + r16) & 1)) v0 = v1 = v2 = v3 = 0.0f;
     }
     if (q0 + r16 < a.Qn) store4<Op>(a, q0 + r16, p, v0, v1, v2, v3);
   }

@@ -513,9 +513,14 @@ __device__ __forceinline__ void gemm_pp_body(const GemmArgs& a, TileOf tile_of, 
 
   // Epilogue: every wave is past its last LDS read; each stages its own
   // 64 rows of C (64 x 256 bytes) through LDS.
+  [[maybe_unused]] uint32_t none = 0u;   // rows with no source
+  if constexpr (GA && Op::BLK != 0) {
+#pragma unroll
+    for (int j = 0; j < TQ; ++j) none |= fqo[j] == kOobOffset ? 1u << j : 0u;
+  }
   staged_epilogue<Op, Cfg::WTP, Cfg::WTQ, TP, TQ, MT, typename Op::Acc16, GA>(
       a, smem + wave * (Cfg::WTQ * 256), acc, Op::BLK != 0 ? lane_id() : lane, p0 + wp * Cfg::WTP,
-      q0 + wq * (Cfg::BQ / 2) + grp * Cfg::WTQ, gt);
+      q0 + wq * (Cfg::BQ / 2) + grp * Cfg::WTQ, gt, none);
   stamp(2);
 }
 

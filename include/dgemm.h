@@ -258,7 +258,8 @@ int gemm_fp8_block(int64_t M, int64_t N, int64_t K, const uint8_t* A, int64_t ld
  *   C[n*ldc + j] = sum_b (sa_rb * sb_ejb) * sum_{k in b} A[r*lda + k] * B[e*group_b + j*ldb + k]
  * A has a factor for each row: sa_rb = scale_a[r * scale_a_row + b * scale_a_block];
  * B one for 128: sb_ejb = scale_b[e * scale_b_group + (j / 128) * scale_b_row + b * scale_b_block].
- * A row whose index is outside 0 .. rows_a - 1 gives zeros.
+ * A row whose index is outside 0 .. rows_a - 1 gives zeros, whatever B and its
+ * factors hold.
  * Checks and limits as gemm_i8_grouped without its counts of factors and its
  * limit of K; negative strides of factors -> DGEMM_ERR_INVALID_LD.
  */

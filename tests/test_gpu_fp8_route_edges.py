@@ -10,7 +10,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_fp8 import FP8, IDS, TYPES, check_quantised, exact, factors, fp8s, gen, kernels, lib, near
+from test_gpu_fp8 import FP8, GROUPED, IDS, TYPES, check_quantised, exact, factors, fp8s, gen, kernels, lib, near
 from test_gpu_route import check
 
 pytestmark = pytest.mark.gpu
@@ -216,6 +216,34 @@ def test_grouped_index_names_rows_twice_and_none():
         c64, mass = exact(a[i:i + 1], b[e], sa[i:i + 1], sb[e])
         near(out[r:r + 1], c64, mass, 300)
     assert bool((out[9] == 3.0).all())          # behind the last group: left
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_grouped_rows_of_no_source_are_zeros_whatever_the_weights_hold(monkeypatch, dtype):
+    """Weights of NaN and factors of infinity and NaN reach the rows that have a source, not those whose index names
+    none, on every kernel."""
+    L = lib()
+    tag = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}[dtype]
+    for name in GROUPED:
+        monkeypatch.setenv("DGEMM_CONFIG", f"b8{tag}_grouped_{name}")
+        for counts, N, K in (([5, 40, 3], 200, 256), ([130, 0, 300], 390, 400), ([1, 1, 1], 64, 100)):
+            g = gen(N)
+            rows = sum(counts)
+            a, sa = fp8s(g, (37, K)), factors(g, 37, K, 1).contiguous()
+            b, sb = fp8s(g, (3, N, K)), torch.stack([factors(g, N, K, 128) for _ in counts]).contiguous()
+            b.view(torch.uint8)[0, 7, 5] = 0x7f
+            sb[0, -1, 0], sb[2, 0, -1], sb[2, -1, 0] = float("inf"), float("nan"), -float("inf")
+            sa[11] = float("nan")
+            index = torch.randint(0, 37, (rows,), generator=g, device="cuda", dtype=torch.int32)
+            index[::3] = torch.tensor([-1, 37, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32, device="cuda")[
+                torch.randint(0, 4, (len(index[::3]),), generator=g, device="cuda")]
+            off = torch.tensor(np.cumsum([0] + counts), dtype=torch.int32, device="cuda")
+            out = torch.full((rows, N), 3.0, dtype=dtype, device="cuda")
+            L.matmul_grouped(a, b, off, sa, sb, out=out, row_index=index)
+            none = (index < 0) | (index >= 37)
+            assert bool((out[none] == 0).all()), name
+            some = torch.arange(rows, device="cuda") < counts[0]     # of the first expert
+            assert bool(torch.isnan(out[some & ~none][:, 7]).all()), name
 
 
 # ---- places past 2^32 ---------------------------------------------------------------
