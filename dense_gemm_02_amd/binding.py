@@ -306,13 +306,16 @@ def _dtype_name(t):
 def _block_factors(a, b, scale_a, scale_b, odt):
     """Whether a product's scale factors are those of blocks: matrices that
     are not vectors of 1 or M (N) factors in another shape.  (With one block
-    of k both say the same; an output type other than float32 is for blocks.)"""
+    of k both say the same; an output type other than float32 is for blocks.
+    Those of 128 rows on both sides can hold M and N values: their shapes tell.)"""
     import torch
     if getattr(a, "dtype", None) != torch.float8_e4m3fn or getattr(scale_a, "ndim", 1) != 2 or \
             getattr(scale_b, "ndim", 1) != 2 or a.ndim != 2 or b.ndim != 2:
         return False
-    M, K = a.shape
-    if scale_a.numel() not in (1, M) or scale_b.numel() not in (1, b.shape[1]):
+    (M, K), N = a.shape, b.shape[1]
+    if scale_a.numel() not in (1, M) or scale_b.numel() not in (1, N):
+        return True
+    if K > 128 and scale_a.shape == (-(-M // 128), -(-K // 128)) and scale_b.shape == (-(-K // 128), -(-N // 128)):
         return True
     return K <= 128 and odt not in (None, torch.float32)
 
@@ -331,7 +334,8 @@ def matmul(a, b, out=None, scale_a=None, scale_b=None, stream=None, out_dtype=No
     with factors of blocks of 128 k (``quantize_fp8``) take them as matrices,
     scale_a of M or ceil(M / 128) rows and ceil(K / 128) columns, scale_b
     turned as b is, ceil(K / 128) rows and N or ceil(N / 128) columns, and
-    give ``out_dtype`` as int8 does.
+    give ``out_dtype`` as int8 does; with more than one block of k one of the
+    two has to be for each row (column): ``gemm_fp8_block`` takes any pair.
     ``out`` may be given with the same layout and dtype.
     """
     import torch

@@ -4,6 +4,7 @@ points document.  No kernel is launched here."""
 import os
 
 import pytest
+import torch
 
 
 @pytest.fixture(scope="module")
@@ -46,3 +47,18 @@ def test_row_counts_near_the_end_of_64_bits(lib):
                                       1, 1, None) == UNSUP
     assert lib.gemm_fp8_grouped(1, 1, 2 ** 31 - 1, 128, FAKE, 1, 128, None, FAKE, 128, 0, FAKE, 2 ** 31, 2, FAKE, 1, 1,
                                 FAKE, 1, 1, 1, FAKE, None) == UNSUP
+
+
+def test_factors_of_128_rows_on_both_sides_are_not_taken_for_vectors():
+    """With as many blocks of k as rows and columns, the factors of blocks on both sides hold M and N values."""
+    from dense_gemm_02_amd.binding import _block_factors
+    for M, N, K in ((64, 64, 8192), (16, 16, 2048), (16, 16, 2047), (2, 2, 129), (16384, 16384, 16384), (16384, 128, 16384)):
+        a, b = (torch.empty((1,), dtype=torch.float8_e4m3fn).expand(shape) for shape in ((M, K), (K, N)))
+        blocks = -(-K // 128)
+        sa, sb = torch.ones((-(-M // 128), blocks)), torch.ones((blocks, -(-N // 128)))
+        assert sa.numel() == M and sb.numel() == N
+        for dtype in (None, torch.float32, torch.bfloat16):
+            assert _block_factors(a, b, sa, sb, dtype)
+        # Vectors in two dimensions are vectors.
+        assert not _block_factors(a, b, torch.ones((M, 1)), torch.ones((1, N)), None)
+        assert not _block_factors(a, b, torch.ones((1, 1)), torch.ones((1, 1)), None)

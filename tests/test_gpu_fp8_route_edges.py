@@ -157,6 +157,18 @@ def test_factors_of_128_rows_on_both_sides(monkeypatch, layout):
         near(c.t() if layout == "tn" else c, c64, mass, K)
 
 
+def test_matmul_refuses_factors_of_128_rows_on_both_sides():
+    """Whatever their number of values: they are never read as one for each row."""
+    L = lib()
+    for M, N, K in ((64, 64, 8192), (16, 16, 2048), (300, 200, 400)):
+        g = gen(M)
+        a, b = fp8s(g, (M, K)), fp8s(g, (N, K))
+        sa, sb = factors(g, M, K, 128), factors(g, N, K, 128)
+        for dtype in TYPES:
+            with pytest.raises(ValueError, match="one for each row"):
+                L.matmul(a, b.t(), scale_a=sa, scale_b=sb.t(), out_dtype=dtype)
+
+
 def test_quantize_into_part_of_a_matrix():
     L = lib()
     x = torch.randn((130, 200), generator=gen(5), device="cuda")
