@@ -358,12 +358,19 @@ def matmul(a, b, out=None, scale_a=None, scale_b=None, stream=None, out_dtype=No
     N = b.shape[1]
     if a.stride(1) != 1 and M * K > 1:
         raise ValueError("a must be row-major (stride(1) == 1)")
-    lda = a.stride(0) if M > 1 else max(K, 1)
+    # The pitch of a single row, whose stride says nothing: its length, with scale
+    # factors (quantize_fp8's results) rounded up to 16 bytes.
+    al = 1 if scale_a is None else 16
+
+    def single(n):
+        return -(-max(n, 1) // al) * al
+
+    lda = a.stride(0) if M > 1 else single(K)
     # (A vector as K x 1, strides (1, 1): a column contiguous along K.)
     if b.stride(1) == 1 and (b.stride(0) != 1 or (N == 1 and K <= 1)):
-        layout, ldb = "nn", (b.stride(0) if K > 1 else max(N, 1))
+        layout, ldb = "nn", (b.stride(0) if K > 1 else single(N))
     elif b.stride(0) == 1:
-        layout, ldb = "tn", (b.stride(1) if N > 1 else max(K, 1))
+        layout, ldb = "tn", (b.stride(1) if N > 1 else single(K))
     else:
         raise ValueError("b must be row-major or column-major")
     odt = torch.float32 if dt in ("f32", "fp8") else a.dtype

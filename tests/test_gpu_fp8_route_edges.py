@@ -10,7 +10,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_fp8 import FP8, GROUPED, IDS, TYPES, check_quantised, exact, factors, fp8s, gen, kernels, lib, near
+from test_gpu_fp8 import FP8, GROUPED, IDS, TYPES, WIDE, check_quantised, exact, factors, fp8s, gen, kernels, lib, near
 from test_gpu_route import check
 
 pytestmark = pytest.mark.gpu
@@ -155,6 +155,25 @@ def test_factors_of_128_rows_on_both_sides(monkeypatch, layout):
         c = torch.full((N, M) if layout == "tn" else (M, N), 7.0, dtype=torch.bfloat16, device="cuda")
         L.gemm_fp8_block(layout, M, N, K, A, a.stride(0), B, ldb, c, ldc, sa, sb)
         near(c.t() if layout == "tn" else c, c64, mass, K)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_matmul_of_single_rows_and_columns_of_any_width(dtype):
+    """One token, one channel, one k, straight from the quantisation, whose pitch a single row's stride does not say."""
+    L = lib()
+    for K in (1, 17, 100, 112, 127, 128, 129, 300):
+        for M, N in ((1, 70), (50, 1), (1, 1), (1, 200), (20, 30)):
+            g = gen(K)
+            x, w = torch.randn((M, K), generator=g, device="cuda"), torch.randn((N, K), generator=g, device="cuda")
+            for ba, bb in ((1, 128), (1, 1)):
+                a, sa = L.quantize_fp8(x, block_rows=ba)
+                b, sb = L.quantize_fp8(w, block_rows=bb)
+                c64, mass = exact(a, b, sa, sb)
+                near(L.matmul(a, b.t(), scale_a=sa, scale_b=sb.t(), out_dtype=dtype), c64, mass, K, WIDE)
+                bt, sbt = L.quantize_fp8(w.t(), block_rows=128) if bb == 128 else (None, None)
+                if bt is not None:                          # row-major: its factors are those of blocks of k as well
+                    c64, mass = exact(a, bt.t(), sa, sbt.t())
+                    near(L.matmul(a, bt, scale_a=sa, scale_b=sbt, out_dtype=dtype), c64, mass, K, WIDE)
 
 
 def test_matmul_refuses_factors_of_128_rows_on_both_sides():
