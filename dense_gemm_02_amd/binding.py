@@ -306,7 +306,8 @@ def _dtype_name(t):
 def _block_factors(a, b, scale_a, scale_b, odt):
     """Whether a product's scale factors are those of blocks: matrices that
     are not vectors of 1 or M (N) factors in another shape.  (With one block
-    of k both say the same; an output type other than float32 is for blocks.
+    of k both say the same; an output type other than float32 is for blocks,
+    and so are factors that are not contiguous, as vectors have to be.
     Those of 128 rows on both sides can hold M and N values: their shapes tell.)"""
     import torch
     if getattr(a, "dtype", None) != torch.float8_e4m3fn or getattr(scale_a, "ndim", 1) != 2 or \
@@ -317,7 +318,7 @@ def _block_factors(a, b, scale_a, scale_b, odt):
         return True
     if K > 128 and scale_a.shape == (-(-M // 128), -(-K // 128)) and scale_b.shape == (-(-K // 128), -(-N // 128)):
         return True
-    return K <= 128 and odt not in (None, torch.float32)
+    return K <= 128 and not (odt in (None, torch.float32) and scale_a.is_contiguous() and scale_b.is_contiguous())
 
 
 def matmul(a, b, out=None, scale_a=None, scale_b=None, stream=None, out_dtype=None):

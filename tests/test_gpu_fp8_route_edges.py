@@ -176,6 +176,20 @@ def test_matmul_of_single_rows_and_columns_of_any_width(dtype):
                     near(L.matmul(a, bt, scale_a=sa, scale_b=sbt, out_dtype=dtype), c64, mass, K, WIDE)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_matmul_takes_factors_of_any_stride_with_one_block_of_k(dtype):
+    """A column of a larger matrix of factors, as with more blocks of k."""
+    L = lib()
+    for M, N, K in ((50, 70, 100), (130, 300, 128), (1, 70, 17), (50, 1, 16)):
+        g = gen(M)
+        a, b = fp8s(g, (M, K)), fp8s(g, (N, K))
+        for ba, bb in ((1, 1), (1, 128), (128, 1)):
+            sa, sb = factors(g, M, K + 256, ba).contiguous()[:, 1:2], factors(g, N, K + 256, bb).contiguous()[:, 2:3]
+            c64, mass = exact(a, b, sa, sb)
+            near(L.matmul(a, b.t(), scale_a=sa, scale_b=sb.t(), out_dtype=dtype), c64, mass, K)
+            near(L.matmul(a, b.t(), scale_a=sa.contiguous(), scale_b=sb.t(), out_dtype=dtype), c64, mass, K)
+
+
 def test_matmul_refuses_factors_of_128_rows_on_both_sides():
     """Whatever their number of values: they are never read as one for each row."""
     L = lib()
