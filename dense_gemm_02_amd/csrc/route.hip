@@ -315,8 +315,9 @@ __device__ __forceinline__ void merge_two(float& one, float& two, float o1, floa
 // The logits come in whole lines, lane after lane, and through LDS to their lanes,
 // four words between those of neighbouring lanes that take V each.
 template <int V>
-struct RowLds {
+struct alignas(16) RowLds {
   static constexpr int N = 20 * V > 16 * V + 64 ? 20 * V : 16 * V + 64;
+  static_assert(N % 4 == 0, "every token's row begins at sixteen bytes");
   float l[4][N], bias[N];
   __device__ static int at(int e) { return e + e / V * 4; }
 };
@@ -621,6 +622,7 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteArgs a) {
     RowLds<V> row;
     WaveLds<WV> wave;
   };
+  static_assert(alignof(Lds) >= 16, "route_row reads sixteen bytes at a time");
   __shared__ Lds lds[4];
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * 4;   // (a wave's LDS is its own: no barrier)
@@ -721,6 +723,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const RouteArgs a) {
 template <class T, int V>
 __global__ void __launch_bounds__(256) route_grad_rows_kernel(const RouteArgs a) {
   using Lds = RowLds<V>;
+  static_assert(alignof(Lds) >= 16, "read and written sixteen bytes at a time");
   __shared__ Lds all[4];
   Lds& lds = all[threadIdx.x >> 6];
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
