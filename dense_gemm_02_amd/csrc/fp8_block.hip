@@ -56,15 +56,35 @@ Launch grouped_launch(int c_type, int kind, bool gather, bool kt) {
                                                     : b8_grouped_bf16(kind, gather, kt));
 }
 
+// The TN strip that DGEMM_CONFIG names (sweeps and tests): its kernel's name with its
+// rows, few rows and stages in flight behind, "b8bf16_tn_skinny_a:32x16x2".
+bool forced_strip(const char* want, int c_type, int64_t Pn, int64_t Qn, Launch* L) {
+  for (int sf = 1; sf <= 2; ++sf)
+    for (int ff = 1; ff <= 4; ff *= 2)
+      for (int stages = 1; stages <= 2; ++stages)
+        for (int few_p = 0; few_p < 2; ++few_p) {
+          if (ff == 4 && (sf == 1 || stages == 2)) continue;   // (not built)
+          *L = skinny_launch(c_type, sf, ff, few_p != 0, stages == 2);
+          char name[64];
+          snprintf(name, sizeof name, "%s:%dx%dx%d", L->name, 16 * sf, 16 * ff, stages);
+          if (strcmp(name, want) == 0)
+            return tiles_of(Pn, L->bp) * tiles_of(Qn, L->bq) <= (double)(0xffffffffll / L->threads);
+        }
+  return false;
+}
+
 // The kernel of a TN product of Pn x Qn x K; `rows`: P has a factor for each row.
 Launch choose_tn(int c_type, int64_t Pn, int64_t Qn, int64_t K, bool rows) {
   const char* want = getenv("DGEMM_CONFIG");
   const bool kt = K % kBlock != 0;
-  if (want != nullptr && *want != 0)
+  if (want != nullptr && *want != 0) {
+    Launch L;
+    if (forced_strip(want, c_type, Pn, Qn, &L)) return L;
     for (int tile = 0; tile < kB8TnTiles; ++tile) {
-      const Launch L = tn_launch(c_type, tile, rows, kt);
+      L = tn_launch(c_type, tile, rows, kt);
       if (strcmp(L.name, want) == 0) return L;
     }
+  }
   // Strips, as for int8 (i8.hip): time in rows fetched per CU.
   const bool few_p = Pn <= Qn;
   const int64_t few = few_p ? Pn : Qn, many = few_p ? Qn : Pn;

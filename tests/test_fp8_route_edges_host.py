@@ -1,6 +1,7 @@
 """Host-only checks of the ends of what the block-scaled FP8 and router entry
 points document.  No kernel is launched here."""
 
+import ctypes
 import os
 
 import pytest
@@ -47,6 +48,25 @@ def test_row_counts_near_the_end_of_64_bits(lib):
                                       1, 1, None) == UNSUP
     assert lib.gemm_fp8_grouped(1, 1, 2 ** 31 - 1, 128, FAKE, 1, 128, None, FAKE, 128, 0, FAKE, 2 ** 31, 2, FAKE, 1, 1,
                                 FAKE, 1, 1, 1, FAKE, None) == UNSUP
+
+
+def test_every_kernel_of_few_rows_can_be_named(lib, monkeypatch):
+    """DGEMM_CONFIG takes the strips with their rows, few rows and stages of copies: kernels that sizes choose rarely can
+    be tested."""
+    buf = ctypes.create_string_buffer(256)
+    for tag, c in (("f32", 0), ("f16", 1), ("bf16", 2)):
+        for order in "ab":
+            for rows, few, stages in ((16, 16, 1), (16, 16, 2), (16, 32, 1), (16, 32, 2), (32, 16, 1), (32, 16, 2),
+                                      (32, 32, 1), (32, 32, 2), (32, 64, 1)):
+                monkeypatch.setenv("DGEMM_CONFIG", f"b8{tag}_tn_skinny_{order}:{rows}x{few}x{stages}")
+                assert lib.dgemm_fp8_block_config(c, 1, 128, 1, 700, 700, 4111, buf, 256) == 0
+                tile = f"{few}x{rows}" if order == "a" else f"{rows}x{few}"
+                lds = max(8 * stages * ((rows + few) * 128 + 512), 4 * 8 * rows * few)
+                assert buf.value.decode().startswith(f"b8{tag}_tn_skinny_{order} tile={tile} threads=512 lds={lds} ")
+    for none in ("b8bf16_tn_skinny_a:16x64x1", "b8bf16_tn_skinny_a:32x64x2", "b8bf16_tn_skinny_b:16x16x3"):
+        monkeypatch.setenv("DGEMM_CONFIG", none)
+        assert lib.dgemm_fp8_block_config(2, 1, 128, 1, 8192, 8192, 8192, buf, 256) == 0
+        assert buf.value.decode().startswith("b8bf16_tn_256x256_pp ")
 
 
 def test_factors_of_128_rows_on_both_sides_are_not_taken_for_vectors():

@@ -10,7 +10,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_fp8 import FP8, GROUPED, IDS, TYPES, WIDE, check_quantised, exact, factors, fp8s, gen, kernels, lib, near
+from test_gpu_fp8 import FP8, GROUPED, IDS, TYPES, WIDE, check_quantised, exact, factors, fp8s, gen, kernels, lib, near, \
+    product
 from test_gpu_route import check
 
 pytestmark = pytest.mark.gpu
@@ -200,6 +201,49 @@ def test_matmul_refuses_factors_of_128_rows_on_both_sides():
         for dtype in TYPES:
             with pytest.raises(ValueError, match="one for each row"):
                 L.matmul(a, b.t(), scale_a=sa, scale_b=sb.t(), out_dtype=dtype)
+
+
+STRIPS = [(order, rows, few, stages) for order in "ab" for rows, few, depth in
+          ((16, 16, 2), (16, 32, 2), (32, 16, 2), (32, 32, 2), (32, 64, 1)) for stages in range(1, depth + 1)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("strip", STRIPS, ids=lambda s: "{}-{}x{}-{}".format(*s))
+def test_every_strip_of_few_rows(monkeypatch, strip, dtype):
+    """TN strips against either operand as the few rows, with one and two stages of copies in flight: fewer stages than
+    waves and many more, K whole, ending inside a block and inside a chunk of 16, ragged strips on both sides."""
+    import ctypes
+    h = lib().load_library()
+    order, rows, few, stages = strip
+    tag = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}[dtype]
+    name = f"b8{tag}_tn_skinny_{order}"
+    monkeypatch.setenv("DGEMM_CONFIG", f"{name}:{rows}x{few}x{stages}")
+    buf = ctypes.create_string_buffer(256)
+    assert h.dgemm_fp8_block_config(TYPES.index(dtype), 1, 1, 128, 700, 700, 700, buf, 256) == 0
+    tile = f"{few}x{rows}" if order == "a" else f"{rows}x{few}"
+    lds = max(8 * stages * ((rows + few) * 128 + 512), 4 * 8 * rows * few)
+    assert buf.value.decode().startswith(f"{name} tile={tile} threads=512 lds={lds} "), buf.value
+    for i, (M, N, K) in enumerate(((1, 1, 1), (33, 130, 129), (130, 33, 512), (64, 64, 1000), (129, 70, 2048),
+                                   (70, 129, 2315), (31, 200, 4111), (200, 31, 5000))):
+        for ba, bb in ((128, 1), (1, 128), (1, 1)):
+            if K > 128 or dtype != torch.float32:            # (one block, FP32 results: the path of vectors)
+                product(gen(i), "tn", M, N, K, ba, bb, dtype, order="rows" if i % 2 else "blocks")
+
+
+def test_strips_chosen_by_size():
+    """Sizes that take strips of their own accord, many rows on either side."""
+    import ctypes
+    h = lib().load_library()
+    buf = ctypes.create_string_buffer(256)
+    seen = set()
+    for i, (M, N, K) in enumerate(((7788, 1, 2315), (57, 1813, 6839), (3507, 62, 2909), (354, 1220, 300), (7362, 44, 300),
+                                   (8192, 16, 8192), (16, 8192, 8192), (20, 5000, 2100), (5000, 40, 2100), (40, 5000, 2100),
+                                   (300, 17, 4096), (17, 300, 4096), (600, 33, 700), (33, 600, 700))):
+        assert h.dgemm_fp8_block_config(2, 1, 128, 1, M, N, K, buf, 256) == 0
+        seen.add(" ".join(buf.value.decode().split()[:4]))
+        product(gen(200 + i), "tn", M, N, K, 128, 1, torch.bfloat16)
+        product(gen(300 + i), "tn", M, N, K, 1, 128, torch.float16, every=True)
+    assert sum("skinny" in s for s in seen) >= 8, seen
 
 
 def test_quantize_into_part_of_a_matrix():
