@@ -42,6 +42,47 @@ def test_scores_that_are_equal_in_64_bits_stand_by_their_logits(score, groups, k
         assert torch.equal(ids.long(), torch.where(mask, logits, -3e38).argsort(dim=1, descending=True, stable=True)[:, :k])
 
 
+def by_logits(logits, k, groups=1, top_groups=1):
+    """The k largest logits, of equal ones the lower index first, of the groups that hold the largest."""
+    l = logits.double() + 0.0
+    if top_groups < groups:
+        T, E = l.shape
+        stay = l.reshape(T, groups, E // groups).amax(2).argsort(dim=1, descending=True, stable=True)[:, :top_groups]
+        mask = torch.zeros((T, groups), dtype=torch.bool, device="cuda").scatter_(1, stay, True)
+        l = torch.where(mask.repeat_interleave(E // groups, 1), l, -3e38)
+    return l.argsort(dim=1, descending=True, stable=True)[:, :k]
+
+
+# (experts, groups, top_groups, k) of routers that take a whole wave a token: sixteen choices and more, more than 256
+# experts, more than sixteen groups, more than sixteen experts for each lane of a group.
+WAVES = [(32, 1, 1, 16), (32, 1, 1, 17), (32, 4, 2, 16), (64, 4, 2, 20), (320, 1, 1, 4), (320, 4, 2, 13), (1024, 1, 1, 64),
+         (96, 32, 9, 7), (252, 12, 5, 8)]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("router", WAVES, ids=lambda r: "{}-{}-{}-{}".format(*r))
+def test_a_wave_a_token_chooses_by_the_logits(router, score):
+    """Sigmoids of 40 and more, softmax shares 800 below the largest, equal in 64 bits; zeros of either sign."""
+    L = lib()
+    E, groups, top_groups, k = router
+    T = 9
+    base = torch.arange(E, device="cuda", dtype=torch.float32)
+    logits = torch.stack([(base * 7 + 5 * t) % E for t in range(T)]) + 40.0          # (7 and E: no common divisor, or 252)
+    if score == "softmax":
+        logits = torch.where(logits == logits.amax(1, keepdim=True), 0.0, logits - 1900.0)
+    kw = dict(score=score, groups=groups, top_groups=top_groups)
+    for renormalize in (True, False):
+        ids, w = L.expert_route(logits, k, renormalize=renormalize, **kw)
+        assert torch.equal(ids.long(), by_logits(logits, k, groups, top_groups))
+        assert bool(torch.isfinite(w).all())
+    zeros = torch.zeros((T, E), device="cuda")
+    zeros[:, ::2] = -0.0
+    zeros[3:6, 1::3] = 1.0
+    zeros[6:, 2::5] = -1.0
+    ids, _ = check(zeros, k, dweights=torch.randn((T, k), generator=gen(E), device="cuda"), **kw)
+    assert torch.equal(ids.long(), by_logits(zeros, k, groups, top_groups))
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("depth", [20.0, 60.0, 84.0, 92.0, 100.0, 110.0])
 def test_groups_of_tiny_scores(score, depth):
