@@ -43,6 +43,7 @@ struct RouteArgs {
 };
 
 constexpr float kInf = __builtin_inff();
+constexpr float kMax = 3.402823466e38f;
 
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
@@ -162,7 +163,6 @@ __device__ __forceinline__ void route_wave(const RouteArgs& a, int64_t t, WaveLd
   top = wave_max(top);
   // A NaN (or, for a softmax, +infinity) leaves no weights.
   const bool bad = __ballot(nan) != 0 || (!a.sigmoid && top == kInf);
-  constexpr float kMax = 3.402823466e38f;
   const double dtop = __builtin_fminf(top, kMax);
 
   double s[V], sum = 0.0;
@@ -440,7 +440,8 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, int64_t t0, RowLds
       if (part + d < lpg) merge_two(b1, b2, u1, u2);
       if (part - d >= 0) merge_two(b1, b2, d1, d2);
     }
-    const float mine = g >= a.groups ? -kInf : (a.group_best == 2 && b2 > -kInf ? b1 + b2 : b1);
+    // (A sum below FP32's range is its lowest value: -infinity is a group with no expert.)
+    const float mine = g >= a.groups ? -kInf : (a.group_best == 2 && b2 > -kInf ? __builtin_fmaxf(b1 + b2, -kMax) : b1);
     // Groups of larger value (of equal ones, lower), each seen by its first lane.
     // (The others show NaN, which is neither.)
     int larger = 0;

@@ -42,6 +42,26 @@ def test_scores_that_are_equal_in_64_bits_stand_by_their_logits(score, groups, k
         assert torch.equal(ids.long(), torch.where(mask, logits, -3e38).argsort(dim=1, descending=True, stable=True)[:, :k])
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("sign", [-1.0, 1.0], ids=["lowest", "highest"])
+def test_biases_at_the_ends_of_float32(score, sign):
+    """Experts masked by the lowest value of float32 (or lifted by the highest): the sum of a group's two best is past
+    float32's range, and the group still counts."""
+    end = sign * float(torch.finfo(torch.float32).max)
+    for E, G, tg, k in ((32, 8, 4, 12), (6, 2, 1, 3), (21, 7, 6, 11), (256, 8, 4, 8), (96, 32, 9, 7)):
+        g = gen(E)
+        logits = torch.randn((40, E), generator=g, device="cuda")
+        size = E // G
+        bias = torch.linspace(-0.1, 0.1, E, device="cuda")
+        bias[size:] = end                                   # one group as it is
+        check(logits, k, bias=bias, score=score, groups=G, top_groups=tg, group_best=2)
+        bias = torch.where(torch.rand((E,), generator=g, device="cuda") < 0.6, end, 0.0)
+        check(logits, k, bias=bias, score=score, groups=G, top_groups=tg, group_best=2)
+        for _ in range(20):
+            bias = sign * torch.rand((E,), generator=g, device="cuda") * 3.4e38
+            check(logits, k, bias=bias, score=score, groups=G, top_groups=tg, group_best=2)
+
+
 def by_logits(logits, k, groups=1, top_groups=1):
     """The k largest logits, of equal ones the lower index first, of the groups that hold the largest."""
     l = logits.double() + 0.0
