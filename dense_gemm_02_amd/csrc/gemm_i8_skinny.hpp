@@ -96,7 +96,7 @@ __device__ __forceinline__ void gemm_i8_skinny_body(const GemmArgs& a, const Gat
     if constexpr (GA) ffo = lane < Cfg::FR ? gather_row(gt, lane, fn, fr * 4, 0) : kOobOffset;
     else if (lane < frows) ffo = (uint32_t)((lane >> fs) * fr * 4);
   }
-  // Few rows with a source, a bit each: the others are zeros (see staged_epilogue).
+  // Few rows with a source, a bit each: the others are zeros (see clear_rows).
   [[maybe_unused]] const uint64_t sources = BLK && GA ? __ballot(ffo != kOobOffset) : 0;
 
   // This wave's stages: every NW-th, from a place that differs between

@@ -511,16 +511,18 @@ __device__ __forceinline__ void gemm_pp_body(const GemmArgs& a, TileOf tile_of, 
   }
   if (grp == 0) barrier();
 
-  // Epilogue: every wave is past its last LDS read; each stages its own
-  // 64 rows of C (64 x 256 bytes) through LDS.
-  [[maybe_unused]] uint32_t none = 0u;   // rows with no source
   if constexpr (GA && Op::BLK != 0) {
+    uint32_t none = 0u;   // rows with no source
 #pragma unroll
     for (int j = 0; j < TQ; ++j) none |= fqo[j] == kOobOffset ? 1u << j : 0u;
+    clear_rows(acc, none);
   }
+
+  // Epilogue: every wave is past its last LDS read; each stages its own
+  // 64 rows of C (64 x 256 bytes) through LDS.
   staged_epilogue<Op, Cfg::WTP, Cfg::WTQ, TP, TQ, MT, typename Op::Acc16, GA>(
       a, smem + wave * (Cfg::WTQ * 256), acc, Op::BLK != 0 ? lane_id() : lane, p0 + wp * Cfg::WTP,
-      q0 + wq * (Cfg::BQ / 2) + grp * Cfg::WTQ, gt, none);
+      q0 + wq * (Cfg::BQ / 2) + grp * Cfg::WTQ, gt);
   stamp(2);
 }
 

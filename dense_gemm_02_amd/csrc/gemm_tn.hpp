@@ -204,7 +204,7 @@ __device__ __forceinline__ void gemm_tn_body(const GemmArgs& a, TileOf tile_of, 
       }
     }
   }
-  // GA and BLK: this lane's rows with no source (see staged_epilogue), looked up among
+  // GA and BLK: this lane's rows with no source (see clear_rows), looked up among
   // the first copies (8192 rows of 64 experts, N 2048, K 4096 199.5 us; ahead of the
   // epilogue 201).
   [[maybe_unused]] uint32_t absent = 0u;
@@ -787,9 +787,6 @@ __device__ __forceinline__ void gemm_tn_body(const GemmArgs& a, TileOf tile_of, 
           // and copy every accumulator each stage.)
           asm("" : "+v"(v0), "+v"(v1), "+v"(v2), "+v"(v3));
           if constexpr (Op::SCALED) sc.apply(fp[gg], j, v0, v1, v2, v3);
-          if constexpr (GA && Op::BLK != 0) {
-            if (absent >> j & 1u) v0 = v1 = v2 = v3 = 0.0f;
-          }
           store4<Op>(a, q, p, v0, v1, v2, v3);
         }
       }
@@ -815,6 +812,7 @@ __device__ __forceinline__ void gemm_tn_body(const GemmArgs& a, TileOf tile_of, 
   if constexpr (Op::BLK != 0) {
 #pragma unroll
     for (int u = NROLL - (Cfg::RING - 1); u < NROLL; ++u) retire(u, fcur);
+    if constexpr (GA) clear_rows(acc, absent);
   }
   // Copies issued past the tile read zeros; let them land before the LDS is
   // reused and before exit.
@@ -831,7 +829,7 @@ __device__ __forceinline__ void gemm_tn_body(const GemmArgs& a, TileOf tile_of, 
     static_assert(!Cfg::STAGED_EPI || Cfg::WTQ * 256 * NW <= 2 * Cfg::STAGE, "staging fits in the stage buffers");
     staged_epilogue<Op, Cfg::WTP, Cfg::WTQ, TP, TQ, MT, Acc, GA>(
         a, smem + wave_u * (Cfg::WTQ * 256), acc, lane_id(), tp * Cfg::BP + wp * Cfg::WTP,
-        tq * Cfg::BQ + wq * Cfg::WTQ, gt, absent);
+        tq * Cfg::BQ + wq * Cfg::WTQ, gt);
   } else {
     direct_epilogue(tile);
   }
