@@ -231,10 +231,10 @@ int quantize_i8(int64_t rows, int64_t K, const void* X, int64_t ldx, int x_type,
  * toward zero, at 2^(E - 13), E the largest sum of the exponents of two values
  * among the products of its eight neighbours along k that are not zero, where
  * a subnormal value has the exponent -6, as in gemm_fp8: less than 7 * 2^-10 of
- * the eight's sum of magnitudes, without subnormal values 7 * 2^-13), the factors' product rounded to FP32 and the
- * sum over blocks by FP32 fused multiply-adds in the order of b (a kernel that
- * splits K over its waves adds their sums in FP32 at the end), rounded once to
- * c_type (a dgemm_type).  Any K: the last block may be shorter, and what lies
+ * the eight's sum of magnitudes, without subnormal values 7 * 2^-13), the
+ * factors' product rounded to FP32 and the sum over blocks by FP32 fused
+ * multiply-adds in the order of b (a kernel that splits K over its waves adds
+ * their sums in FP32 at the end), rounded once to c_type (a dgemm_type).  Any K: the last block may be shorter, and what lies
  * behind K in a row's last 16 bytes is not used.
  * sa_ib is scale_a[(i / rows_a) * scale_a_row + b * scale_a_block], and
  * sb_jb is scale_b[(j / rows_b) * scale_b_row + b * scale_b_block] (j: column
